@@ -7,6 +7,7 @@ in Python.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -79,7 +80,6 @@ def workspace(nbytes: int, device) -> torch.Tensor:
 
 
 def device_status(ws: torch.Tensor) -> int:
-    import ctypes
     v = ctypes.c_int32(0)
     call("moe_get_device_status", ws.data_ptr(), ctypes.addressof(v), _stream())
     return v.value
@@ -245,6 +245,126 @@ def moe_aux_loss(probs, bins, K: int, alpha: float, ws=None):
     call("moe_aux_loss", _p(probs), _p(bins), N, K, E, float(alpha), _p(loss), _p(P), ws.data_ptr(),
          ws.numel(), _stream())
     return loss, P
+
+
+def _same_device(named) -> torch.device:
+    """The CUDA device every given tensor lives on."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensors must live on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
+    return dev
+
+
+def _call_on(dev: torch.device, name: str, *args) -> None:
+    """Call an entry point on `dev` and its current stream, whichever device is current."""
+    if dev.index == torch.cuda.current_device():
+        call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+def moe_add_rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None):
+    """h = x + residual (h = x without one), y = h / sqrt(mean(h^2) + eps) * weight; returns (y, h).
+
+    x, residual [N, H], weight [H].  y and h may be given, also to work in place
+    (h = residual or x, y = x or residual, two different buffers).
+    """
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [N, H], got {tuple(x.shape)}")
+    N, H = x.shape
+    dt = _dt(x)
+    _check("weight", weight, (H,), x.dtype)
+    _check("residual", residual, (N, H), x.dtype)
+    _check("y", y, (N, H), x.dtype)
+    _check("h", h, (N, H), x.dtype)
+    if h is not None and residual is None:
+        raise ValueError("h: without a residual h is x itself")
+    dev = _same_device((("x", x), ("weight", weight), ("residual", residual), ("y", y), ("h", h)))
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if residual is not None and h is None:
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if h is not None and N > 0 and h.data_ptr() == y.data_ptr():
+        raise ValueError("y and h must be different buffers")
+    _call_on(dev, "moe_add_rms_norm", _p(x), _p(residual), _p(weight), N, H, dt, float(eps), _p(h), _p(y))
+    return y, (x if residual is None else h)
+
+
+def moe_add_rms_norm_bwd(dy, h, weight, dh=None, eps: float = 1e-6, dx=None, dweight=None, ws=None):
+    """Gradients of moe_add_rms_norm: (dx, dweight).  h is the forward's; dh is the gradient
+    that reaches h past the norm.  dx is the gradient of x and of residual alike."""
+    if dy.dim() != 2:
+        raise ValueError(f"dy: expected [N, H], got {tuple(dy.shape)}")
+    N, H = dy.shape
+    dt = _dt(dy)
+    _check("h", h, (N, H), dy.dtype)
+    _check("weight", weight, (H,), dy.dtype)
+    _check("dh", dh, (N, H), dy.dtype)
+    _check("dx", dx, (N, H), dy.dtype)
+    _check("dweight", dweight, (H,), dy.dtype)
+    dev = _same_device((("dy", dy), ("h", h), ("weight", weight), ("dh", dh), ("dx", dx), ("dweight", dweight),
+                        ("ws", ws)))
+    if dx is None:
+        dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
+    if dweight is None:
+        dweight = torch.empty(H, dtype=dy.dtype, device=dev)
+    if ws is None:
+        ws = torch.empty(load().moe_add_rms_norm_bwd_workspace_size(N, H, dt), dtype=torch.uint8, device=dev)
+    _call_on(dev, "moe_add_rms_norm_bwd", _p(dy), _p(h), _p(weight), _p(dh), N, H, dt, float(eps), _p(dx),
+             _p(dweight), _p(ws), ws.numel())
+    return dx, dweight
+
+
+def clip_workspace(grads) -> torch.Tensor:
+    """A workspace for moe_clip_grad_norm over a list of this many tensors, on their device."""
+    grads = list(grads)
+    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    return torch.empty(load().moe_clip_grad_norm_workspace_size(len(grads)), dtype=torch.uint8, device=dev)
+
+
+def moe_clip_grad_norm(grads, max_norm: float, outs=None, ws=None, norm=None) -> torch.Tensor:
+    """Scale the gradients to a global norm of at most max_norm, in place or into `outs`;
+    returns the norm they had, a float32 tensor [1] on their device.
+
+    grads: contiguous float32 or bfloat16 CUDA tensors of one device, which may share no memory.
+    A list without tensors needs `ws` or `norm` to name the device, or takes the current one.
+    """
+    grads = list(grads)
+    n = len(grads)
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError(f"outs: expected {n} tensors, got {len(outs)}")
+    _check("norm", norm, (1,), torch.float32)
+    ptrs, sizes, dts = [], [], []
+    for i, g in enumerate(grads):
+        dts.append(_dt(g))
+        sizes.append(g.numel())
+        if outs is not None:
+            _check(f"outs[{i}]", outs[i], tuple(g.shape), g.dtype)
+    dev = _same_device([("grads", g) for g in grads] + [("outs", o) for o in outs or ()] +
+                       [("ws", ws), ("norm", norm)])
+    if dev is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    ptrs = [_p(g) for g in grads]
+    outp = [_p(o) for o in outs] if outs is not None else None
+    if ws is None:
+        ws = torch.empty(load().moe_clip_grad_norm_workspace_size(n), dtype=torch.uint8, device=dev)
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    _call_on(dev, "moe_clip_grad_norm", (ctypes.c_void_p * n)(*ptrs) if n else None,
+             (ctypes.c_void_p * n)(*outp) if n and outp is not None else None,
+             (ctypes.c_int64 * n)(*sizes) if n else None, (ctypes.c_int32 * n)(*dts) if n else None,
+             n, float(max_norm), _p(norm), _p(ws), ws.numel())
+    return norm
 
 
 def selftest_wait_timeout(status, timeout_ns: int):

@@ -339,6 +339,59 @@ moe_status moe_layer_bwd(const void* dy, const void* x, const void* W_r, const v
 moe_status moe_sum_rank_ordered(const void* shards, int32_t n_ranks, int64_t numel, moe_dtype dt,
                                 float scale, void* out, moe_stream_t stream);
 
+/* Residual addition and root-mean-square norm, the step before the router in
+ * a transformer block (the layer's x is its y):
+ *   h[n] = round(x[n] + residual[n])          (residual NULL: h = x, and the
+ *                                              argument h is neither read nor written)
+ *   y[n] = round(h[n] * s_n * weight),  s_n = 1 / sqrt(mean_j h[n][j]^2 + eps)
+ * y is the norm of h as rounded to dt, the value the backward reads.  Sums and
+ * the normalisation run in fp32.
+ *   x, residual, h, y [N,H]; weight [H] (all dt); eps >= 0.
+ * In place: h may be residual or x, y may be x or residual (not both outputs
+ * the same buffer); any other overlap is undefined.
+ * H: a multiple of 8 up to 16384 (bf16), of 4 up to 8192 (fp32). */
+moe_status moe_add_rms_norm(const void* x, const void* residual, const void* weight, int32_t N, int32_t H,
+                            moe_dtype dt, float eps, void* h, void* y, moe_stream_t stream);
+
+/* Its gradient.  With g = dy * weight and xhat = h * s (s as above):
+ *   dx[n]   = round(s_n * (g[n] - xhat[n] * mean_j(g[n][j] xhat[n][j])) + dh[n])
+ *   dweight = round(sum_n dy[n] * xhat[n])    (fixed order, fp32)
+ * dh [N,H] is the gradient that reaches h past the norm (the residual stream),
+ * NULL for none; dx is the gradient of x and of residual alike.
+ *   dy, h, dh, dx [N,H]; weight, dweight [H] (all dt).  dx may be dy, h or dh.
+ *   N = 0: dweight is zeroed.  H as above.
+ * ws: moe_add_rms_norm_bwd_workspace_size bytes (never less for more rows; 0
+ * for a shape the call would reject); it needs no moe_workspace_init. */
+size_t moe_add_rms_norm_bwd_workspace_size(int32_t N, int32_t H, moe_dtype dt);
+moe_status moe_add_rms_norm_bwd(const void* dy, const void* h, const void* weight, const void* dh, int32_t N,
+                                int32_t H, moe_dtype dt, float eps, void* dx, void* dweight, void* ws,
+                                size_t ws_bytes, moe_stream_t stream);
+
+/* Global norm of `count` gradients and their scaling to at most max_norm
+ * (after the data-parallel sum and before the optimiser):
+ *   *norm = sqrt(sum_i sum_j grads[i][j]^2)              (device float)
+ *   outs[i][j] = round(grads[i][j] * f),  f = min(1, max_norm / (*norm + 1e-6))
+ * grads, outs, numels, dtypes: HOST arrays of `count` entries, read before
+ * the call returns; their pointers are device pointers aligned to their
+ * element (16-byte aligned ones, with outs[i] at the same offset from a
+ * 16-byte boundary as grads[i], are read and written in 16-byte vectors).
+ * dtypes[i]: a moe_dtype, which may differ from tensor to tensor.
+ * outs NULL: in place (nothing is written when f = 1).  outs[i] may be
+ * grads[i]; two written ranges that overlap, or one that overlaps another
+ * gradient, are MOE_ERR_INVALID_ARG.  Empty tensors are skipped; an empty
+ * list has norm 0.
+ * max_norm >= 0; infinity only takes the norm.  A norm of infinity gives
+ * f = 0, a NaN norm makes every gradient NaN, as the formula has it: test *norm.
+ * Sums run in fp32 within 16 KB chunks and in double beyond, in a fixed order;
+ * the norm is right whenever it is a float, also where squares are not.
+ * Two launches for up to 768 tensors.  Capturable.
+ * ws: moe_clip_grad_norm_workspace_size(count) bytes (never less for more
+ * tensors); it needs no moe_workspace_init. */
+size_t moe_clip_grad_norm_workspace_size(int32_t count);
+moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                              const int32_t* dtypes, int32_t count, float max_norm, float* norm, void* ws,
+                              size_t ws_bytes, moe_stream_t stream);
+
 /* Diagnostics (no counterpart on the pages): one block waits, with the same
  * bounded mbarrier wait every tcgen05 GEMM pipeline stage uses, on a barrier
  * that nothing arrives at; after timeout_ns (1 us .. 1 s) it gives up and

@@ -1,0 +1,155 @@
+"""Global gradient norm and clipping against the formula in 64 bits (GPU only).
+
+Tolerances.  u = 2^-24.  A thread adds at most 32 positive squares in fp32 and
+the rest runs in double: the sum is off by less than 33 u, the norm by less
+than 17 u with its own rounding, the factor by less than 18 u; a scaled gradient by
+one product's rounding more and the store's.
+"""
+import math
+
+import pytest
+import torch
+
+import dropless_top_moe_b200 as moe
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def rand(shape, dtype, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def norm64(grads):
+    return math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+
+
+def check(norm, outs, grads, max_norm):
+    n = norm64(grads)
+    assert norm.shape == (1,) and norm.dtype == torch.float32
+    assert abs(float(norm) - n) <= 17 * U * n
+    f = min(1.0, max_norm / (n + 1e-6))
+    for o, g in zip(outs, grads):
+        want = g.double() * f
+        tol = want.abs() * (torch.finfo(g.dtype).eps / 2 + 20 * U) + torch.finfo(g.dtype).tiny
+        assert o.dtype == g.dtype and bool(((o.double() - want).abs() <= tol).all())
+
+
+LISTS = {
+    "one": [(7,)],
+    "layer": [(128, 4), (4, 128, 256), (4, 128, 256), (4, 256, 128), (128,)],
+    "odd": [(1,), (3,), (8,), (9,), (4095,), (4096,), (4097,), (333, 1001), (0,), (5, 0, 2), (17,)],
+    "large": [(64, 512, 300), (1 << 22,)],
+    "many": [(i % 37 + 1, 19) for i in range(1700)],      # several launches of the longest table
+    "hundred": [(513,)] * 100,
+}
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mixed"])
+@pytest.mark.parametrize("name", sorted(LISTS))
+def test_clips_to_the_norm(name, kind):
+    dts = {"f32": [torch.float32], "bf16": [torch.bfloat16], "mixed": [torch.float32, torch.bfloat16]}[kind]
+    grads = [rand(s, dts[i % len(dts)], i) for i, s in enumerate(LISTS[name])]
+    keep = [g.clone() for g in grads]
+    n = norm64(grads)
+    outs = [torch.empty_like(g) for g in grads]
+    norm = moe.moe_clip_grad_norm(grads, 0.3 * n, outs=outs)
+    check(norm, outs, keep, 0.3 * n)
+    assert all(torch.equal(g, k) for g, k in zip(grads, keep))
+    again = [torch.empty_like(g) for g in grads]
+    norm2 = moe.moe_clip_grad_norm(grads, 0.3 * n, outs=again)
+    assert torch.equal(norm, norm2) and all(torch.equal(a, b) for a, b in zip(outs, again))
+    norm3 = moe.moe_clip_grad_norm(grads, 0.3 * n)                   # in place
+    assert torch.equal(norm, norm3) and all(torch.equal(a, b) for a, b in zip(outs, grads))
+
+
+def test_below_the_limit_nothing_changes():
+    grads = [rand((1000,), torch.bfloat16, 1), rand((77, 3), torch.float32, 2)]
+    keep = [g.clone() for g in grads]
+    outs = [torch.zeros_like(g) for g in grads]
+    for limit in (2 * norm64(grads), math.inf):
+        norm = moe.moe_clip_grad_norm(grads, limit, outs=outs)
+        check(norm, outs, keep, limit)
+        assert all(torch.equal(o, k) for o, k in zip(outs, keep))
+        moe.moe_clip_grad_norm(grads, limit)
+        assert all(torch.equal(g, k) for g, k in zip(grads, keep))
+
+
+def test_offset_views():
+    """Views of one buffer that start and end off the 16-byte boundaries, the neighbours untouched."""
+    for dt in (torch.float32, torch.bfloat16):
+        flat = rand((40000,), dt, 3)
+        keep = flat.clone()
+        cuts = [(1, 2), (3, 4), (5, 12), (13, 5000), (5001, 5001 + 8191), (14001, 39999)]
+        grads = [flat[a:b] for a, b in cuts]
+        ref = [g.clone() for g in grads]
+        n = norm64(ref)
+        outflat = torch.full((40003,), 7.0, dtype=dt, device="cuda")
+        outs = [outflat[a + 3:b + 3] for a, b in cuts]           # another offset than the inputs
+        check(moe.moe_clip_grad_norm(grads, 0.5 * n, outs=outs), outs, ref, 0.5 * n)
+        check(moe.moe_clip_grad_norm(grads, 0.5 * n), grads, ref, 0.5 * n)
+        mask = torch.ones(40000, dtype=torch.bool, device="cuda")
+        for a, b in cuts:
+            mask[a:b] = False
+        assert torch.equal(flat[mask], keep[mask])
+        assert bool((outflat[3:][mask] == 7.0).all()) and bool((outflat[:3] == 7.0).all())
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-22, 1e-12, 1e12, 1e22, 1e30])
+def test_norms_whose_squares_leave_the_range(scale):
+    grads = [rand((5000,), torch.float32, 1, scale), rand((5000,), torch.bfloat16, 2, scale),
+             torch.zeros(9000, device="cuda")]
+    n = norm64(grads)
+    outs = [torch.empty_like(g) for g in grads]
+    check(moe.moe_clip_grad_norm(grads, 0.25 * n, outs=outs), outs, grads, 0.25 * n)
+
+
+def test_a_large_and_small_gradients_together():
+    grads = [torch.full((3000,), 1e-25, device="cuda"), torch.full((3,), 1e20, device="cuda")]
+    outs = [torch.empty_like(g) for g in grads]
+    check(moe.moe_clip_grad_norm(grads, 1.0, outs=outs), outs, grads, 1.0)
+
+
+def test_values_that_are_not_finite():
+    g = rand((5000,), torch.float32, 1)
+    g[17] = float("inf")
+    out = torch.empty_like(g)
+    norm = moe.moe_clip_grad_norm([g], 1.0, outs=[out])
+    assert math.isinf(float(norm)) and bool(out[17].isnan()) and bool((out[:17] == 0).all())
+    g[17] = float("nan")
+    norm = moe.moe_clip_grad_norm([g], 1.0, outs=[out])
+    assert math.isnan(float(norm)) and bool(out.isnan().all())
+
+
+def test_empty_lists():
+    assert float(moe.moe_clip_grad_norm([], 1.0)) == 0.0
+    assert float(moe.moe_clip_grad_norm([torch.zeros(0, device="cuda")], 1.0)) == 0.0
+
+
+def test_a_limit_of_zero():
+    g = rand((100,), torch.float32, 1)
+    out = torch.ones_like(g)
+    moe.moe_clip_grad_norm([g], 0.0, outs=[out])
+    assert bool((out == 0).all())
+
+
+def test_replays_from_a_graph_with_new_gradients():
+    grads = [rand((300, 70), torch.bfloat16, 1), rand((9999,), torch.float32, 2)]
+    outs = [torch.empty_like(g) for g in grads]
+    ws = moe.clip_workspace(grads)
+    norm = torch.zeros(1, device="cuda")
+    moe.moe_clip_grad_norm(grads, 1.0, outs=outs, ws=ws, norm=norm)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        moe.moe_clip_grad_norm(grads, 1.0, outs=outs, ws=ws, norm=norm)
+    for k in range(3):
+        for i, g in enumerate(grads):
+            g.copy_(rand(g.shape, g.dtype, 10 * k + i, 0.1 + k))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(norm, outs, grads, 1.0)

@@ -1,0 +1,117 @@
+"""Refusals of the norm, clipping and few-token entry points (CPU only: the
+checks run before any device work, so pointers are never dereferenced)."""
+import ctypes
+
+import pytest
+import torch
+
+import dropless_top_moe_b200 as moe
+from dropless_top_moe_b200._lib import (MOE_BF16, MOE_ERR_INVALID_ARG as INV, MOE_ERR_UNSUPPORTED as UNS,
+                                        MOE_ERR_WORKSPACE as WS, MOE_F32, load)
+
+bf, f32 = torch.bfloat16, torch.float32
+BIG = 1 << 40
+A, B, C, D, E_ = (0x100000000 * (i + 1) for i in range(5))   # aligned, far apart, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dropless_top_moe_b200.build import build
+    build()
+    return load()
+
+
+def z(*shape, dtype=bf):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def test_norm_refuses(lib):
+    def fwd(x=A, r=B, w=C, N=16, H=128, dt=MOE_BF16, eps=1e-6, h=D, y=E_):
+        return lib.moe_add_rms_norm(x, r, w, N, H, dt, eps, h, y, None)
+    assert fwd(x=None) == INV and fwd(w=None) == INV and fwd(y=None) == INV
+    assert fwd(h=None) == INV                          # a residual needs somewhere to keep the sum
+    assert fwd(x=A + 2) == INV and fwd(h=D + 8) == INV
+    assert fwd(dt=2) == INV and fwd(N=-1) == INV and fwd(H=0) == INV
+    assert fwd(eps=-1.0) == INV and fwd(eps=float("nan")) == INV
+    assert fwd(H=12) == UNS and fwd(H=6, dt=MOE_F32) == UNS
+    assert fwd(H=16392) == UNS and fwd(H=8196, dt=MOE_F32) == UNS
+    assert fwd(h=E_) == INV                            # both outputs the same
+    assert fwd(y=A + 256) == INV and fwd(h=B + 16) == INV and fwd(y=C - 256) == INV   # partial overlaps
+
+
+def test_norm_backward_refuses(lib):
+    def bwd(dy=A, h=B, w=C, dh=None, N=16, H=128, dt=MOE_BF16, eps=1e-6, dx=D, dw=E_, ws=6 * A, n=BIG):
+        return lib.moe_add_rms_norm_bwd(dy, h, w, dh, N, H, dt, eps, dx, dw, ws, n, None)
+    assert bwd(dy=None) == INV and bwd(h=None) == INV and bwd(w=None) == INV
+    assert bwd(dx=None) == INV and bwd(dw=None) == INV
+    assert bwd(ws=None) == WS and bwd(n=256) == WS
+    assert bwd(dx=A + 16) == INV and bwd(dw=C) == INV and bwd(dw=D + 256) == INV
+    assert bwd(H=4) == UNS and bwd(eps=-0.5) == INV and bwd(dh=A + 1) == INV
+    size = lib.moe_add_rms_norm_bwd_workspace_size
+    assert size(16, 12, MOE_BF16) == 0 and size(-1, 128, MOE_BF16) == 0
+    last = 0
+    for N in (0, 1, 2, 100, 148, 500, 3000, 1 << 20, 2 ** 31 - 1):     # never less for more rows
+        assert size(N, 2048, MOE_F32) >= max(last, 256)
+        last = size(N, 2048, MOE_F32)
+
+
+def test_clip_refuses(lib):
+    def clip(ptrs=(A, B), outs=None, sizes=(100, 100), dts=(MOE_F32, MOE_BF16), max_norm=1.0, norm=C, ws=D, n=BIG):
+        k = len(ptrs)
+        return lib.moe_clip_grad_norm((ctypes.c_void_p * k)(*ptrs),
+                                      None if outs is None else (ctypes.c_void_p * k)(*outs),
+                                      (ctypes.c_int64 * k)(*sizes), (ctypes.c_int32 * k)(*dts), k, max_norm, norm,
+                                      ws, n, None)
+    assert clip(ptrs=(A, None)) == INV and clip(ptrs=(A + 2, B)) == INV and clip(ptrs=(A, B + 1)) == INV
+    assert clip(sizes=(100, -1)) == INV and clip(dts=(0, 7)) == INV
+    assert clip(max_norm=-1.0) == INV and clip(max_norm=float("nan")) == INV
+    assert clip(norm=None) == INV and clip(ws=None) == WS and clip(n=300) == WS and clip(ws=D + 4) == INV
+    assert clip(ptrs=(A, A)) == INV                           # the same gradient twice
+    assert clip(ptrs=(A, A + 396)) == INV                     # its last element shared
+    assert clip(outs=(C, C + 200)) == INV                     # outputs that overlap
+    assert clip(outs=(A + 16, C)) == INV                      # an output over its own gradient, shifted
+    assert clip(outs=(B, C)) == INV                           # an output over another gradient
+    assert clip(outs=(C, None)) == INV and clip(outs=(C + 1, D)) == INV
+    assert lib.moe_clip_grad_norm(None, None, None, None, 3, 1.0, C, D, BIG, None) == INV
+    assert lib.moe_clip_grad_norm(None, None, None, None, -1, 1.0, C, D, BIG, None) == INV
+    assert lib.moe_clip_grad_norm_workspace_size(-1) == 0
+    assert lib.moe_clip_grad_norm_workspace_size(769) > lib.moe_clip_grad_norm_workspace_size(768) > 256
+
+
+def test_binding_checks_the_norms_tensors():
+    x, w = z(4, 128), z(128)
+    with pytest.raises(ValueError, match="x"):
+        moe.moe_add_rms_norm(z(2, 4, 128), w)
+    with pytest.raises(ValueError, match="weight"):
+        moe.moe_add_rms_norm(x, z(64))
+    with pytest.raises(TypeError, match="weight"):
+        moe.moe_add_rms_norm(x, z(128, dtype=f32))
+    with pytest.raises(ValueError, match="residual"):
+        moe.moe_add_rms_norm(x, w, residual=z(5, 128))
+    with pytest.raises(ValueError, match="h"):
+        moe.moe_add_rms_norm(x, w, h=z(4, 128))
+    with pytest.raises(TypeError, match="dtype"):
+        moe.moe_add_rms_norm(z(4, 128, dtype=torch.float16), z(128, dtype=torch.float16))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_add_rms_norm(x, w)
+    with pytest.raises(ValueError, match="dh"):
+        moe.moe_add_rms_norm_bwd(x, x, w, dh=z(4, 64))
+    with pytest.raises(ValueError, match="dweight"):
+        moe.moe_add_rms_norm_bwd(x, x, w, dweight=z(64))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_add_rms_norm_bwd(x, x, w)
+
+
+def test_binding_checks_the_gradients():
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_clip_grad_norm([z(4)], 1.0)
+    with pytest.raises(TypeError, match="dtype"):
+        moe.moe_clip_grad_norm([z(4, dtype=torch.float64)], 1.0)
+    with pytest.raises(ValueError, match="outs"):
+        moe.moe_clip_grad_norm([z(4)], 1.0, outs=[])
+    with pytest.raises(ValueError, match=r"outs\[0\]"):
+        moe.moe_clip_grad_norm([z(4)], 1.0, outs=[z(5)])
+    with pytest.raises(TypeError, match=r"outs\[0\]"):
+        moe.moe_clip_grad_norm([z(4)], 1.0, outs=[z(4, dtype=f32)])
+    with pytest.raises(TypeError, match="norm"):
+        moe.moe_clip_grad_norm([z(4)], 1.0, norm=z(1))
