@@ -48,6 +48,9 @@ SIGNATURES = {
                             FL, FL, P, P, P, P, P, P, SZ, P]),
     "moe_dispatch_meta_noalloc": (I32, [P, I32, I32, I32, P, P, P, P, P, P, P]),
     "moe_sum_rank_ordered": (I32, [P, I32, I64, I32, FL, P, P]),
+    "moe_decode_max_tokens": (I32, []),
+    "moe_layer_decode_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
+    "moe_layer_decode": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I32, P, P, P, P, SZ, P]),
     "moe_add_rms_norm": (I32, [P, P, P, I32, I32, I32, FL, P, P, P]),
     "moe_add_rms_norm_bwd_workspace_size": (SZ, [I32, I32, I32]),
     "moe_add_rms_norm_bwd": (I32, [P, P, P, P, I32, I32, I32, FL, P, P, P, SZ, P]),

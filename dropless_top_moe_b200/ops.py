@@ -460,3 +460,55 @@ class MoELayer:
 
     def status(self) -> int:
         return device_status(self.ws)
+
+
+class MoEDecodeLayer:
+    """The layer for up to N tokens at a time (a decoding step), through moe_layer_decode.
+
+    forward() takes any number of tokens up to N.  After a call, top_experts and weights hold its
+    routing.  The outputs are the layer's own buffers, overwritten by the next call.
+    """
+
+    def __init__(self, N: int, H: int, E: int, K: int, F: int, dtype=torch.bfloat16, device="cuda"):
+        if dtype not in _DT:
+            raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+        self.N, self.H, self.E, self.K, self.F = N, H, E, K, F
+        self.dtype, self.dt = dtype, _DT[dtype]
+        nbytes = load().moe_layer_decode_workspace_size(N, H, E, K, F, self.dt)
+        if nbytes == 0:
+            raise _lib.MoEError("moe_layer_decode_workspace_size", _lib.MOE_ERR_UNSUPPORTED)
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        with torch.cuda.device(dev):
+            self.ws = workspace(nbytes, dev)
+        self.y = torch.empty(N, H, dtype=dtype, device=dev)
+        self._top = torch.empty(N, K, dtype=torch.int32, device=dev)
+        self._weights = torch.empty(N, K, dtype=torch.float32, device=dev)
+        self.top_experts, self.weights = self._top, self._weights
+
+    def forward(self, x, W_r, W1, W3, W2, y=None):
+        H, E, F, dt = self.H, self.E, self.F, self.dtype
+        if x.dim() != 2 or x.shape[0] > self.N:
+            raise ValueError(f"x: expected at most {self.N} rows of {H}, got {tuple(x.shape)}")
+        n = x.shape[0]
+        _check("x", x, (n, H), dt)
+        _check("W_r", W_r, (H, E), dt)
+        _check("W1", W1, (E, H, F), dt)
+        _check("W3", W3, (E, H, F), dt)
+        _check("W2", W2, (E, F, H), dt)
+        _check("y", y, (n, H), dt)
+        for name, t in (("x", x), ("W_r", W_r), ("W1", W1), ("W3", W3), ("W2", W2), ("y", y)):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name}: on {t.device}, the layer on {self.device}")
+        if y is None:
+            y = self.y[:n]
+        self.top_experts, self.weights = self._top[:n], self._weights[:n]
+        _call_on(self.device, "moe_layer_decode", _p(x), _p(W_r), _p(W1), _p(W3), _p(W2), n, H, E, self.K, F, self.dt,
+                 _p(y), self._top.data_ptr(), self._weights.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+        return y
+
+    def status(self) -> int:
+        with torch.cuda.device(self.device):
+            return device_status(self.ws)

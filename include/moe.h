@@ -339,6 +339,29 @@ moe_status moe_layer_bwd(const void* dy, const void* x, const void* W_r, const v
 moe_status moe_sum_rank_ordered(const void* shards, int32_t n_ranks, int64_t numel, moe_dtype dt,
                                 float scale, void* out, moe_stream_t stream);
 
+/* The whole layer for a few tokens (a decoding step), forward only: route,
+ * select, the selected experts' SwiGLU and the weighted sum in two launches,
+ * with the same weights and formulas as moe_layer_fwd but no padded expert
+ * groups, so the time is the reading of the selected experts' weights.
+ *   x, y [N,H] (dt), N <= moe_decode_max_tokens(); top_experts [N,K] int32;
+ *   weights [N,K] float32.  y may be x; no other overlap.
+ * Sums run in fp32; bf16 layers round the activations once to bf16 between the
+ * two products, and y is rounded once (the expert outputs stay in fp32, so y
+ * can differ in the last bit from moe_layer_fwd's).  The same inputs give the
+ * same bits on every call, and a token's outputs depend on its own row only up
+ * to the order of fp32 sums.  A NaN logit ranks like -infinity.
+ * Shapes: K <= E <= 256, K <= 32; bf16: H and F multiples of 128; fp32: H a
+ * multiple of 4, any F; H, F <= 2^20.
+ * ws: moe_layer_decode_workspace_size bytes for this N or a larger one, the
+ * other sizes equal; zeroed once with moe_workspace_init.  Calls that share a
+ * workspace must be ordered on the GPU; calls on different ones may overlap. */
+int32_t moe_decode_max_tokens(void);
+size_t moe_layer_decode_workspace_size(int32_t N, int32_t H, int32_t E, int32_t K, int32_t F, moe_dtype dt);
+moe_status moe_layer_decode(const void* x, const void* W_r, const void* W1, const void* W3, const void* W2,
+                            int32_t N, int32_t H, int32_t E, int32_t K, int32_t F, moe_dtype dt, void* y,
+                            int32_t* top_experts, float* weights, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
+
 /* Residual addition and root-mean-square norm, the step before the router in
  * a transformer block (the layer's x is its y):
  *   h[n] = round(x[n] + residual[n])          (residual NULL: h = x, and the

@@ -115,3 +115,32 @@ def test_binding_checks_the_gradients():
         moe.moe_clip_grad_norm([z(4)], 1.0, outs=[z(4, dtype=f32)])
     with pytest.raises(TypeError, match="norm"):
         moe.moe_clip_grad_norm([z(4)], 1.0, norm=z(1))
+
+
+def test_few_token_layer_refuses(lib):
+    def dec(x=A, W_r=B, W1=C, W3=D, W2=E_, N=16, H=128, E=4, K=2, F=256, dt=MOE_BF16, y=6 * A, top=7 * A, w=8 * A,
+            ws=9 * A, n=BIG):
+        return lib.moe_layer_decode(x, W_r, W1, W3, W2, N, H, E, K, F, dt, y, top, w, ws, n, None)
+    for k in ("x", "W_r", "W1", "W3", "W2", "y", "top", "w"):
+        assert dec(**{k: None}) == INV, k
+        assert dec(**{k: 10 * A + 4}) == INV, k
+    assert dec(ws=None) == WS and dec(n=1000) == WS and dec(ws=9 * A + 8) == INV
+    assert dec(dt=5) == INV and dec(N=-1) == INV and dec(K=5) == INV and dec(K=0) == INV and dec(F=0) == INV
+    assert dec(N=lib.moe_decode_max_tokens() + 1) == UNS
+    assert dec(H=192) == UNS and dec(F=100) == UNS and dec(E=257) == UNS and dec(E=64, K=33) == UNS
+    assert dec(dt=MOE_F32, H=130) == UNS and dec(F=(1 << 20) + 128) == UNS
+    size = lib.moe_layer_decode_workspace_size
+    assert size(16, 192, 4, 2, 256, MOE_BF16) == 0 and size(129, 128, 4, 2, 256, MOE_BF16) == 0
+    for dt in (MOE_BF16, MOE_F32):                       # one workspace serves every smaller batch
+        for H, E, K, F in ((128, 4, 2, 256), (4096, 64, 4, 2048), (7168, 256, 8, 2048), (4096, 8, 2, 14336)):
+            last = 0
+            for N in range(0, 129):
+                assert size(N, H, E, K, F, dt) >= max(last, 256), (N, H)
+                last = size(N, H, E, K, F, dt)
+
+
+def test_binding_checks_the_few_token_layers_tensors():
+    with pytest.raises(moe.MoEError):
+        moe.MoEDecodeLayer(8, 100, 4, 2, 256)
+    with pytest.raises(TypeError, match="dtype"):
+        moe.MoEDecodeLayer(8, 128, 4, 2, 256, dtype=torch.float16)
