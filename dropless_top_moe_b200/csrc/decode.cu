@@ -38,7 +38,7 @@ decode_route_kernel(const Args a, int S, int EP) {
   pdl_launch();
   const int tid = threadIdx.x, g = blockIdx.y, s = blockIdx.x;
   if (s == 0 && g == 0)
-    for (int i = tid; i < (int)(sizeof(Counters) / sizeof(int)); i += kRouteThreads) ((int*)a.cnt)[i] = 0;
+    for (int i = tid; i < a.zero_ints; i += kRouteThreads) ((int*)a.cnt)[i] = 0;
   const T* x = (const T*)a.x;
   const T* wr = (const T*)a.W_r;
   const int E = a.E, H = a.H;
@@ -346,8 +346,8 @@ moe_status check(int N, int H, int E, int K, int F, moe_dtype dt) {
   if (N > kMaxTokens || E > kMaxExperts || K > 32) return MOE_ERR_UNSUPPORTED;
   if (dt == MOE_F32 && H % 4 != 0) return MOE_ERR_UNSUPPORTED;
   if (dt == MOE_BF16 && (H % 128 != 0 || F % 128 != 0)) return MOE_ERR_UNSUPPORTED;
-  // tile counts and element offsets of a workspace row stay within 32 bits
-  if (H > (1 << 20) || F > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  // tile counts, the tensor-core kernel's unit counts and a batch's elements stay within 31 bits
+  if (H > (1 << 16) || F > (1 << 16)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -379,21 +379,37 @@ size_t part_bytes(int N, int H, int E) {
   return most;
 }
 
-size_t carve(Args* a, char* base, int N, int H, int E, int K, int F, moe_dtype dt) {
+// What only the bf16 expert kernel has.
+struct UmmaWs {
+  int* tile_cnt;
+  float* part_up;
+  float* part_down;
+};
+
+size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, moe_dtype dt) {
   size_t off = kStatusBytes;
   auto take = [&](size_t bytes) {
     char* p = base ? base + off : nullptr;
     off += al256(bytes);
     return (void*)p;
   };
-  void* cnt = take(sizeof(Counters));
+  const int64_t used = (int64_t)N * K < E ? (int64_t)N * K : E;
+  const size_t tiles = dt == MOE_BF16 ? (size_t)used * (F / 128) : 0;
+  const size_t zero = sizeof(Counters) + tiles * sizeof(int);
+  void* cnt = take(zero);
   void* part = take(part_bytes(N, H, E));
   void* act = take((size_t)N * K * F * elem(dt));
   void* out = take((size_t)N * K * H * sizeof(float));
+  void* pu = dt == MOE_BF16 ? take(umma_part_bytes(N)) : nullptr;
+  void* pd = dt == MOE_BF16 ? take(umma_part_bytes(N)) : nullptr;
   if (a) {
     a->status = (int*)base;
     a->arrive = (int*)(base + 64);
     a->cnt = (Counters*)cnt;
+    a->zero_ints = (int)(zero / sizeof(int));
+    w->tile_cnt = (int*)((char*)cnt + sizeof(Counters));
+    w->part_up = (float*)pu;
+    w->part_down = (float*)pd;
     a->logit_part = (float*)part;
     a->act = act;
     a->out = (float*)out;
@@ -459,7 +475,7 @@ int32_t moe_decode_max_tokens(void) { return decode::kMaxTokens; }
 
 size_t moe_layer_decode_workspace_size(int32_t N, int32_t H, int32_t E, int32_t K, int32_t F, moe_dtype dt) {
   if (decode::check(N, H, E, K, F, dt) != MOE_OK) return 0;
-  return decode::carve(nullptr, nullptr, N, H, E, K, F, dt);
+  return decode::carve(nullptr, nullptr, nullptr, N, H, E, K, F, dt);
 }
 
 moe_status moe_layer_decode(const void* x, const void* W_r, const void* W1, const void* W3, const void* W2,
@@ -479,11 +495,12 @@ moe_status moe_layer_decode(const void* x, const void* W_r, const void* W1, cons
   a.x = x; a.W_r = W_r; a.W1 = W1; a.W3 = W3; a.W2 = W2;
   a.N = N; a.H = H; a.E = E; a.K = K; a.F = F;
   a.y = y; a.top = top_experts; a.weights = weights;
-  carve(&a, (char*)ws, N, H, E, K, F, dt);
+  UmmaWs w;
+  carve(&a, &w, (char*)ws, N, H, E, K, F, dt);
   cudaStream_t s = (cudaStream_t)stream;
   const moe_status rs = dt == MOE_F32 ? route<float>(a, s) : route<__nv_bfloat16>(a, s);
   if (rs != MOE_OK) return rs;
-  return dt == MOE_F32 ? experts<float>(a, s) : experts<__nv_bfloat16>(a, s);
+  return dt == MOE_F32 ? experts<float>(a, s) : experts_umma(a, w.part_up, w.part_down, w.tile_cnt, s);
 }
 
 }  // extern "C"

@@ -39,10 +39,15 @@ struct Args {
   int* status;
   int* arrive;                 // [kMaxGroups], inside the status region: zero between calls
   Counters* cnt;
+  int zero_ints;               // the router kernel zeroes this many from cnt on
   float* logit_part;           // [groups][S][TG][E]
   void* act;                   // [N*K][F]
   float* out;                  // [N*K][H]
 };
+
+// decode_umma.cu: the expert kernel for bf16
+size_t umma_part_bytes(int N);   // partial sums of one phase
+moe_status experts_umma(const Args& a, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s);
 
 // ---- plan: which experts are used, by which tokens ---------------------------
 // Slots are the used experts in increasing id; a slot's rows are its tokens in

@@ -1,0 +1,600 @@
+// Expert kernel of the few-token layer for bf16: the selected experts' gate/up
+// and down products on tcgen05, the weights streamed once.
+//
+// The products are taken transposed: the weights' columns are the MMA's 128 rows
+// (A, read MN-major as they lie in memory), the expert's tokens its columns
+// (B, 16 to 128 of them), so one token costs no 128-row padding and a weight
+// element passes through shared memory once whatever the number of tokens.
+// With T tokens an expert there are 2 T FLOP a weight byte - far below the
+// tensor cores' rate up to T = 128 - so HBM bounds the kernel: 3 H F bf16
+// weights of every used expert.
+//
+// A unit of work is 64 rows (k) of two 128-column weight tiles: gate and up of
+// the same columns, or two neighbouring tiles of W2; 32 KB either way.  All units of
+// a phase form one line (slot, tile, k) that is cut into tickets of equal length
+// whatever the tiles' borders, so the blocks stream the same number of bytes
+// however few experts are used.  A ticket's piece of a tile that is not the whole
+// tile leaves fp32 partial sums: of gate and up, the piece that arrives last adds the pieces
+// in order and applies SwiGLU; of the down product, the weighted sum over
+// the experts adds them in order while it reads them.  No sum depends on the
+// order in which blocks run.
+//
+// One block an SM, tickets taken in order (decode.cuh says why that cannot
+// deadlock).  Warp 0 takes tickets and streams weights, running up to the whole
+// ring (about 200 KB) ahead: it asks for the down tiles while the activations they
+// meet are still being computed.  Warp 1 brings the tokens' rows: TMA row gathers of
+// x, or rows of the activations once their slot is complete.  Warp 2 issues the MMAs, warps
+// 4-7 read TMEM (two accumulator sets) and write.
+#include <cuda.h>
+#include <string.h>
+
+#include "decode.cuh"
+
+namespace moe {
+namespace decode {
+namespace {
+
+using namespace umma;
+
+constexpr int kBlocks = 148;
+constexpr int kThreads = 256;
+constexpr int kKB = 64;                     // rows of a unit
+constexpr int kABytes = 4 * 8192;           // four 64 x 64 weight boxes
+constexpr int kMaxStages = 6;
+constexpr int kRing = 8;                    // tickets in flight in a block
+constexpr int kSmemData = 210 * 1024;
+constexpr int kPartFloats = 2 * 128;        // a token's sums of one piece
+
+struct Params {
+  CUtensorMap tw1, tw3, tw2;   // [E][H][F], [E][F][H]: 64 x 64 boxes
+  CUtensorMap tx;              // [N][H]: one-row boxes, gathered
+  CUtensorMap tact;            // [N*K][F]: 16-row boxes
+  Args a;
+  float* part_up;              // [2 * tickets][2][N][128]
+  float* part_down;
+  int* tile_cnt;               // [slots][F / 128] pieces that have arrived, zeroed by the router
+  int stages;
+  int b_bytes;                 // of a stage: N rounded up to 16 rows of 128 bytes
+};
+
+// A phase's line of units and its cut into tickets of q units.
+struct Line {
+  int nj, kc;      // tiles of a slot, units of a tile
+  int units, q, tickets;
+};
+// Two tickets a block once each is long; one while a second would only add pieces.
+__device__ __forceinline__ Line make_line(int slots, int nj, int kc) {
+  Line l;
+  l.nj = nj;
+  l.kc = kc;
+  l.units = slots * nj * kc;
+  const int most = l.units >= kBlocks * 64 ? 2 * kBlocks : kBlocks;
+  l.q = (l.units + most - 1) / most;
+  l.tickets = (l.units + l.q - 1) / l.q;
+  return l;
+}
+// A ticket's next piece: units [pos, pos + len) of one tile.
+struct Piece {
+  int tile, k0, len;
+};
+__device__ __forceinline__ Piece piece_at(const Line& l, int pos, int end) {
+  Piece p;
+  p.tile = pos / l.kc;
+  p.k0 = pos - p.tile * l.kc;
+  p.len = l.kc - p.k0 < end - pos ? l.kc - p.k0 : end - pos;
+  return p;
+}
+// Partial-sum entry of ticket t's piece of the tile that starts at unit a.
+__device__ __forceinline__ int entry_of(const Line& l, int t, int a) { return 2 * t + (t * l.q >= a ? 0 : 1); }
+
+struct Ticket {
+  bool up, sum, stop;
+  int t;
+};
+__device__ __forceinline__ Ticket read_ticket(int v, const Line& up, const Line& down, int n_sum) {
+  Ticket k;
+  k.up = v < up.tickets;
+  k.t = k.up ? v : v - up.tickets;
+  k.sum = !k.up && k.t >= down.tickets;
+  if (k.sum) k.t -= down.tickets;
+  k.stop = k.sum && k.t >= n_sum;
+  return k;
+}
+
+__device__ __forceinline__ int round16(int v) { return (v + 15) & ~15; }
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+__device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// All of the epilogue's threads: whether each of them says yes.  Its warps leave
+// together or not at all, since they meet at barriers.
+__device__ __forceinline__ bool epi_all(bool yes) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((int)yes)
+      : "memory");
+  return r != 0;
+}
+
+struct Shared {
+  Plan plan;
+  int tokens[kMaxTokens];      // warp 1's current slot
+  uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages];
+  uint64_t tfull[2], tempty[2];
+  uint64_t ring_full[kRing], ring_empty[kRing];
+  uint64_t drain;
+  int ring[kRing];
+  uint32_t tmem;
+  int abort;
+  int last;
+  int ok;
+};
+
+constexpr int kVecSum = 4;     // columns of y a thread adds up
+
+__global__ void __launch_bounds__(kThreads, 1)
+decode_umma_kernel(const __grid_constant__ Params p) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ Shared sm;
+  const Args& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t stage_bytes = kABytes + p.b_bytes;
+  volatile int* abort_flag = &sm.abort;
+  auto bar = [](const uint64_t& b) { return smem_u32(&b); };
+
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(bar(sm.full_a[i]), 1);
+      mbar_init(bar(sm.full_b[i]), 1);
+      mbar_init(bar(sm.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(sm.tfull[i]), 1);
+      mbar_init(bar(sm.tempty[i]), 4);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar(sm.ring_full[i]), 1);
+      mbar_init(bar(sm.ring_empty[i]), 6);
+    }
+    mbar_init(bar(sm.drain), 1);
+    sm.abort = 0;
+    fence_barrier_init();
+  } else if (warp == 1 && lane < 5) {
+    const CUtensorMap* m[5] = {&p.tw1, &p.tw3, &p.tw2, &p.tx, &p.tact};
+    tma_prefetch_desc(m[lane]);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&sm.tmem), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const Line up = make_line(sm.plan.slots, a.F / 128, a.H / kKB);
+  const Line down = make_line(sm.plan.slots, (a.H + 255) / 256, a.F / kKB);
+  const int vecs = a.N * (a.H / kVecSum);
+  const int n_sum = (vecs + 127) / 128;
+
+  // the roles' view of the ticket ring
+  int slot = 0;
+  uint32_t ring_phase = 0;
+  auto next_slot = [&]() {
+    if (++slot == kRing) { slot = 0; ring_phase ^= 1u; }
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------ tickets and weights
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    int v = 0;
+    if (lane == 0) v = atomicAdd(&a.cnt->ticket, 1);
+    for (;;) {
+      int next = 0;
+      if (lane == 0) {
+        ok = mbar_wait_bounded(bar(sm.ring_empty[slot]), ring_phase ^ 1u, abort_flag, a.status, kTimeoutNs);
+        if (ok) {
+          sm.ring[slot] = v;
+          mbar_arrive(bar(sm.ring_full[slot]));
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      if (!ok) break;
+      const Ticket k = read_ticket(__shfl_sync(0xffffffffu, v, 0), up, down, n_sum);
+      if (k.stop) break;
+      if (lane == 0) next = atomicAdd(&a.cnt->ticket, 1);     // arrives while this one's tiles are asked for
+      next_slot();
+      if (!k.sum) {
+        const Line& l = k.up ? up : down;
+        const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
+        for (int pos = k.t * l.q; pos < end && ok;) {
+          const Piece pc = piece_at(l, pos, end);
+          const int u = pc.tile / l.nj, j = pc.tile - u * l.nj;
+          const int e = sm.plan.expert[u];
+          // lane 0-3: one 64-column box each
+          const CUtensorMap* m = !k.up ? &p.tw2 : (lane < 2 ? &p.tw1 : &p.tw3);
+          const int c = k.up ? j * 128 + (lane & 1) * 64 : j * 256 + lane * 64;
+          for (int i = 0; i < pc.len; ++i) {
+            if (lane == 0) {
+              ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
+              if (ok) mbar_expect_tx(bar(sm.full_a[stage]), kABytes);
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!ok) break;
+            if (lane < 4)
+              tma_load_3d(base + stage * stage_bytes + lane * 8192, m, bar(sm.full_a[stage]), c, (pc.k0 + i) * kKB, e);
+            ++issued;
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+          }
+          pos += pc.len;
+        }
+      }
+      if (!ok) break;
+      v = next;
+    }
+    if (lane == 0) {
+      // the copies in flight land before the block leaves, also after a wait gave up
+      for (int i = 0; i < p.stages && i < issued; ++i) {
+        if (stage-- == 0) { stage = p.stages - 1; phase ^= 1u; }
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(bar(sm.full_a[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
+      }
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------- the tokens' rows
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    int have = -1;                     // slot whose activations are known to be complete
+    while (ok) {
+      if (lane == 0) ok = mbar_wait_bounded(bar(sm.ring_full[slot]), ring_phase, abort_flag, a.status, kTimeoutNs);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      if (!ok) break;
+      const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down, n_sum);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sm.ring_empty[slot]));
+      next_slot();
+      if (k.stop) break;
+      if (k.sum) continue;
+      const Line& l = k.up ? up : down;
+      const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
+      for (int pos = k.t * l.q; pos < end && ok;) {
+        const Piece pc = piece_at(l, pos, end);
+        const int u = pc.tile / l.nj;
+        const int e = sm.plan.expert[u], r0 = sm.plan.off[u], cnt = sm.plan.off[u + 1] - r0, n16 = round16(cnt);
+        int g0 = a.N, g1 = a.N, g2 = a.N, g3 = a.N;        // rows past the last token read as zeros
+        if (k.up) {
+          for (int n = lane; n < a.N; n += 32)
+            if ((sm.plan.mask[e][n >> 5] >> (n & 31)) & 1u) sm.tokens[plan_row(sm.plan, n, e) - r0] = n;
+          __syncwarp();
+          if (4 * lane < cnt) g0 = sm.tokens[4 * lane];
+          if (4 * lane + 1 < cnt) g1 = sm.tokens[4 * lane + 1];
+          if (4 * lane + 2 < cnt) g2 = sm.tokens[4 * lane + 2];
+          if (4 * lane + 3 < cnt) g3 = sm.tokens[4 * lane + 3];
+          __syncwarp();
+        } else if (have != u) {
+          if (lane == 0) {
+            ok = wait_count(a.cnt->done_act + u, up.nj, a.cnt, a.status);
+            if (!ok) *abort_flag = 1;
+          }
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          if (!ok) break;
+          fence_proxy_async_global();                      // written by other threads, read by TMA
+          have = u;
+        }
+        for (int i = 0; i < pc.len; ++i) {
+          if (lane == 0) {
+            ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
+            if (ok) mbar_expect_tx(bar(sm.full_b[stage]), n16 * 128);
+          }
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          if (!ok) break;
+          const uint32_t dst = base + stage * stage_bytes + kABytes;
+          const int kcol = (pc.k0 + i) * kKB;
+          if (k.up) {
+            if (4 * lane < n16) tma_gather4(dst + lane * 512, &p.tx, bar(sm.full_b[stage]), kcol, g0, g1, g2, g3);
+          } else {
+            if (16 * lane < n16) tma_load_2d(dst + lane * 2048, &p.tact, bar(sm.full_b[stage]), kcol, r0 + 16 * lane);
+          }
+          ++issued;
+          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        }
+        pos += pc.len;
+      }
+    }
+    if (lane == 0) {
+      for (int i = 0; i < p.stages && i < issued; ++i) {
+        if (stage-- == 0) { stage = p.stages - 1; phase ^= 1u; }
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(bar(sm.full_b[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
+      }
+    }
+  } else if (warp == 2) {
+    // --------------------------------------------------------------------- MMA
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      while (ok) {
+        ok = mbar_wait_bounded(bar(sm.ring_full[slot]), ring_phase, abort_flag, a.status, kTimeoutNs);
+        if (!ok) break;
+        const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down, n_sum);
+        mbar_arrive(bar(sm.ring_empty[slot]));
+        next_slot();
+        if (k.stop) break;
+        if (k.sum) continue;
+        const Line& l = k.up ? up : down;
+        const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
+        for (int pos = k.t * l.q; pos < end && ok;) {
+          const Piece pc = piece_at(l, pos, end);
+          const int u = pc.tile / l.nj;
+          const int n16 = round16(sm.plan.off[u + 1] - sm.plan.off[u]);
+          const uint32_t idesc = idesc_bf16(128, n16, true, false);
+          ok = mbar_wait_bounded(bar(sm.tempty[acc]), acc_phase ^ 1u, abort_flag, a.status, kTimeoutNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + acc * 256;
+          for (int i = 0; i < pc.len; ++i) {
+            ok = mbar_wait_bounded(bar(sm.full_a[stage]), phase, abort_flag, a.status, kTimeoutNs) &&
+                 mbar_wait_bounded(bar(sm.full_b[stage]), phase, abort_flag, a.status, kTimeoutNs);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = base + stage * stage_bytes, sb = sa + kABytes;
+#pragma unroll
+            for (int kk = 0; kk < kKB / 16; ++kk) {
+              const uint64_t bd = desc_k_sw128(sb + kk * 32);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                mma_bf16(d + h * 128, desc_mn_sw128(sa + h * 16384 + kk * 2048, 8192), bd, idesc,
+                         (i | kk) != 0 ? 1u : 0u);
+            }
+            mma_commit(bar(sm.empty[stage]));
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+          }
+          if (!ok) break;
+          mma_commit(bar(sm.tfull[acc]));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+          pos += pc.len;
+        }
+      }
+      if (*abort_flag) {
+        // the MMAs in flight still read shared memory and write TMEM
+        mma_commit(bar(sm.drain));
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(bar(sm.drain), 0) && globaltimer() - t0 < 50000000ull) {}
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- epilogue
+    const int et = tid - 128, quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    __nv_bfloat16* act = (__nv_bfloat16*)a.act;
+    const size_t entry = (size_t)a.N * kPartFloats;        // floats of a partial-sum entry
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    while (ok) {
+      if (lane == 0) ok = mbar_wait_bounded(bar(sm.ring_full[slot]), ring_phase, abort_flag, a.status, kTimeoutNs);
+      ok = epi_all(ok);
+      if (!ok) break;
+      const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down, n_sum);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sm.ring_empty[slot]));
+      next_slot();
+      if (k.stop) break;
+      if (k.sum) {
+        // y[n] = sum_k w[n,k] out[row(n,k)], k in order, each out from its pieces in order
+        if (lane == 0) {
+          ok = wait_count(&a.cnt->done_down, down.tickets, a.cnt, a.status);
+          if (!ok) *abort_flag = 1;
+        }
+        ok = epi_all(ok);
+        if (!ok) break;
+        const int at = k.t * 128 + et;
+        if (at < vecs) {
+          const int n = at / (a.H / kVecSum), h = (at - n * (a.H / kVecSum)) * kVecSum;
+          const int j = h >> 8;
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < a.K; ++i) {
+            const int e = __ldcg(a.top + n * a.K + i);
+            const float w = __ldcg(a.weights + n * a.K + i);
+            const int u = sm.plan.slot_of[e], row = plan_row(sm.plan, n, e);
+            const int a0 = (u * down.nj + j) * down.kc;
+            const int t0 = a0 / down.q, t1 = (a0 + down.kc - 1) / down.q;
+            float4 o;
+            if (t0 == t1) {
+              o = __ldcg((const float4*)(a.out + (size_t)row * a.H + h));
+            } else {
+              const size_t in = (size_t)((h >> 7) & 1) * a.N * 128 + (size_t)(row - sm.plan.off[u]) * 128 + (h & 127);
+              o = make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int t = t0; t <= t1; ++t) {
+                const float4 q = __ldcg((const float4*)(p.part_down + entry * entry_of(down, t, a0) + in));
+                o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
+              }
+            }
+            s.x = fmaf(w, o.x, s.x); s.y = fmaf(w, o.y, s.y); s.z = fmaf(w, o.z, s.z); s.w = fmaf(w, o.w, s.w);
+          }
+          *(uint2*)((__nv_bfloat16*)a.y + (size_t)n * a.H + h) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+        }
+        continue;
+      }
+      const Line& l = k.up ? up : down;
+      const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
+      for (int pos = k.t * l.q; pos < end;) {
+        const Piece pc = piece_at(l, pos, end);
+        const int u = pc.tile / l.nj, j = pc.tile - u * l.nj;
+        const int r0 = sm.plan.off[u], cnt = sm.plan.off[u + 1] - r0;
+        const bool whole = pc.len == l.kc;
+        if (lane == 0) ok = mbar_wait_bounded(bar(sm.tfull[acc]), acc_phase, abort_flag, a.status, kTimeoutNs);
+        ok = epi_all(ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * 256 + lanes;
+        const int a0 = pc.tile * l.kc;
+        float* part = (k.up ? p.part_up : p.part_down) + entry * entry_of(l, k.t, a0) + et;
+        for (int c = 0; c < cnt; c += 16) {
+          uint32_t v0[16], v1[16];
+          tmem_ld_16(d + c, v0);
+          tmem_ld_16(d + 128 + c, v1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i >= cnt) break;
+            const float f0 = __uint_as_float(v0[i]), f1 = __uint_as_float(v1[i]);
+            if (!whole) {
+              part[(c + i) * 128] = f0;
+              part[((size_t)a.N + c + i) * 128] = f1;
+            } else if (k.up) {
+              act[(size_t)(r0 + c + i) * a.F + j * 128 + et] = __float2bfloat16_rn(silu_f(f0) * f1);
+            } else {
+              float* o = a.out + (size_t)(r0 + c + i) * a.H + j * 256 + et;
+              o[0] = f0;
+              if (j * 256 + 128 < a.H) o[128] = f1;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm.tempty[acc]));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+        if (k.up) {
+          bool finish = whole;
+          if (!whole) {
+            // the last piece of the tile to arrive adds them all
+            const int t0 = a0 / l.q, t1 = (a0 + l.kc - 1) / l.q;
+            __threadfence();
+            epi_barrier();
+            if (et == 0) sm.last = atomicAdd(p.tile_cnt + pc.tile, 1) == t1 - t0;
+            epi_barrier();
+            finish = sm.last != 0;
+            if (finish) {
+              __threadfence();
+              for (int c = 0; c < cnt; ++c) {
+                float g = 0.f, w = 0.f;
+                for (int t = t0; t <= t1; ++t) {
+                  const float* q = p.part_up + entry * entry_of(l, t, a0) + et;
+                  g += __ldcg(q + (size_t)c * 128);
+                  w += __ldcg(q + ((size_t)a.N + c) * 128);
+                }
+                act[(size_t)(r0 + c) * a.F + j * 128 + et] = __float2bfloat16_rn(silu_f(g) * w);
+              }
+            }
+          }
+          if (finish) {
+            fence_proxy_async_global();
+            __threadfence();
+            epi_barrier();
+            if (et == 0) add_release(a.cnt->done_act + u, 1);
+          }
+        }
+        pos += pc.len;
+      }
+      if (!ok) break;
+      if (!k.up) {
+        __threadfence();
+        epi_barrier();
+        if (et == 0) add_release(&a.cnt->done_down, 1);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sm.abort) *(volatile int*)&a.cnt->abort = 1;
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// ---- host --------------------------------------------------------------------
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? (EncodeTiledFn)ptr
+               : (EncodeTiledFn) nullptr;
+  }();
+  return fn;
+}
+
+// bf16 map over [d2][d1][d0] (d0 contiguous), 128-byte swizzle, boxes of box1 x 64.
+bool map3(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1, int rank) {
+  EncodeTiledFn f = encode_fn();
+  if (!f) return false;
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
+  cuuint32_t box[3] = {64, box1, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+size_t umma_part_bytes(int N) { return (size_t)(2 * 2 * kBlocks) * N * kPartFloats * sizeof(float); }
+
+moe_status experts_umma(const Args& a, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s) {
+  Params p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  p.part_up = part_up;
+  p.part_down = part_down;
+  p.tile_cnt = tile_cnt;
+  p.b_bytes = (int)round_up(a.N, 16) * 128;
+  p.stages = kSmemData / (kABytes + p.b_bytes);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  if (!map3(&p.tw1, a.W1, a.F, a.H, a.E, 64, 3) || !map3(&p.tw3, a.W3, a.F, a.H, a.E, 64, 3) ||
+      !map3(&p.tw2, a.W2, a.H, a.F, a.E, 64, 3) || !map3(&p.tx, a.x, a.H, a.N, 1, 1, 2) ||
+      !map3(&p.tact, a.act, a.F, (uint64_t)a.N * a.K, 1, 16, 2))
+    return MOE_ERR_CUDA;
+  const size_t smem = (size_t)p.stages * (kABytes + p.b_bytes) + 1024;
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    if (cudaFuncSetAttribute(decode_umma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemData + 1024) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(kBlocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t err = cudaSuccess;
+  MOE_TRACED("decode_experts_umma", s, (err = cudaLaunchKernelEx(&cfg, decode_umma_kernel, p)));
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // namespace decode
+}  // namespace moe

@@ -351,7 +351,7 @@ moe_status moe_sum_rank_ordered(const void* shards, int32_t n_ranks, int64_t num
  * same bits on every call, and a token's outputs depend on its own row only up
  * to the order of fp32 sums.  A NaN logit ranks like -infinity.
  * Shapes: K <= E <= 256, K <= 32; bf16: H and F multiples of 128; fp32: H a
- * multiple of 4, any F; H, F <= 2^20.
+ * multiple of 4, any F; H, F <= 65536.
  * ws: moe_layer_decode_workspace_size bytes for this N or a larger one, the
  * other sizes equal; zeroed once with moe_workspace_init.  Calls that share a
  * workspace must be ordered on the GPU; calls on different ones may overlap. */

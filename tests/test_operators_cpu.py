@@ -128,7 +128,7 @@ def test_few_token_layer_refuses(lib):
     assert dec(dt=5) == INV and dec(N=-1) == INV and dec(K=5) == INV and dec(K=0) == INV and dec(F=0) == INV
     assert dec(N=lib.moe_decode_max_tokens() + 1) == UNS
     assert dec(H=192) == UNS and dec(F=100) == UNS and dec(E=257) == UNS and dec(E=64, K=33) == UNS
-    assert dec(dt=MOE_F32, H=130) == UNS and dec(F=(1 << 20) + 128) == UNS
+    assert dec(dt=MOE_F32, H=130) == UNS and dec(F=(1 << 16) + 128) == UNS
     size = lib.moe_layer_decode_workspace_size
     assert size(16, 192, 4, 2, 256, MOE_BF16) == 0 and size(129, 128, 4, 2, 256, MOE_BF16) == 0
     for dt in (MOE_BF16, MOE_F32):                       # one workspace serves every smaller batch
