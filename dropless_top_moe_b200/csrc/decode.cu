@@ -26,56 +26,102 @@ namespace moe {
 namespace decode {
 namespace {
 
-constexpr int kRouteThreads = 1024;
-constexpr int kRouteRows = 256;      // rows of x staged at a time
+constexpr int kRouteThreads = 256;
+constexpr int kRouteLoads = 8;       // rows of W_r a thread has in flight
+constexpr int kRouteCols = 1024;     // most (token, expert) sums of a block
 
-template <typename T, int TG>
+// Order of floats as unsigned numbers; NaN ranks like -infinity.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(isnan(v) ? -INFINITY : v);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// W_r columns: V neighbours a thread where E is a whole number of vectors, else one.
+template <typename T, int TG, bool WIDE>
 __global__ void __launch_bounds__(kRouteThreads)
 decode_route_kernel(const Args a, int S, int EP) {
-  __shared__ float xs[TG * kRouteRows];
-  __shared__ float red[kRouteThreads * TG];
+  constexpr int V = WIDE ? Vec<T>::N : 1;
+  __shared__ __align__(16) float xs[kRouteThreads * kRouteLoads / 8][TG];   // chunk rows x tokens
+  __shared__ __align__(16) float red[8 * kRouteCols];
   __shared__ int last;
   pdl_launch();
   const int tid = threadIdx.x, g = blockIdx.y, s = blockIdx.x;
-  if (s == 0 && g == 0)
-    for (int i = tid; i < a.zero_ints; i += kRouteThreads) ((int*)a.cnt)[i] = 0;
+  const int warp = tid >> 5, lane = tid & 31;
   const T* x = (const T*)a.x;
   const T* wr = (const T*)a.W_r;
   const int E = a.E, H = a.H;
   const int t0 = g * TG;
   const int nt = a.N - t0 < TG ? a.N - t0 : TG;
   const int h0 = (int)((int64_t)H * s / S), h1 = (int)((int64_t)H * (s + 1) / S);
-  const int R = kRouteThreads / EP, e = tid % EP, r = tid / EP;
-  float acc[TG];
+  const int CT = EP / V;                       // threads a row: a power of two
+  const int R = kRouteThreads / CT;            // rows a pass
+  const int c = (tid % CT) * V, r = tid / CT;
+  const int chunk = R * kRouteLoads < (int)(sizeof(xs) / sizeof(xs[0])) ? R * kRouteLoads : (int)(sizeof(xs) / sizeof(xs[0]));
+  float acc[TG][V];
 #pragma unroll
-  for (int t = 0; t < TG; ++t) acc[t] = 0.f;
-  for (int c0 = h0; c0 < h1; c0 += kRouteRows) {
-    const int rows = h1 - c0 < kRouteRows ? h1 - c0 : kRouteRows;
-    __syncthreads();
-    for (int i = tid; i < TG * kRouteRows; i += kRouteThreads) {
-      const int t = i / kRouteRows, h = i % kRouteRows;
-      xs[i] = t < nt && h < rows ? to_f<T>(x[(size_t)(t0 + t) * H + c0 + h]) : 0.f;
+  for (int t = 0; t < TG; ++t)
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[t][j] = 0.f;
+  for (int c0 = h0; c0 < h1; c0 += chunk) {
+    const int rows = h1 - c0 < chunk ? h1 - c0 : chunk;
+    // the weights' loads go out before x is staged
+    float w[kRouteLoads][V];
+    uint4 wv[kRouteLoads];
+#pragma unroll
+    for (int i = 0; i < kRouteLoads; ++i) {
+      const int h = r + i * R;
+      const bool in = h < rows && c < E;
+      if (WIDE) {
+        wv[i] = in ? ld_nc_v4(wr + (size_t)(c0 + h) * E + c) : make_uint4(0, 0, 0, 0);
+      } else {
+        w[i][0] = in ? to_f<T>(wr[(size_t)(c0 + h) * E + c]) : 0.f;
+      }
     }
     __syncthreads();
-    if (e < E) {
-#pragma unroll 16
-      for (int h = r; h < rows; h += R) {
-        const float w = to_f<T>(wr[(size_t)(c0 + h) * E + e]);
+    for (int i = tid; i < rows * TG; i += kRouteThreads) {
+      const int t = i / rows, h = i - t * rows;
+      xs[h][t] = t < nt ? to_f<T>(x[(size_t)(t0 + t) * H + c0 + h]) : 0.f;
+    }
+    __syncthreads();
 #pragma unroll
-        for (int t = 0; t < TG; ++t) acc[t] = fmaf(xs[t * kRouteRows + h], w, acc[t]);
+    for (int i = 0; i < kRouteLoads; ++i) {
+      const int h = r + i * R;
+      if (h < rows) {
+        if constexpr (WIDE) Vec<T>::to_float(wv[i], w[i]);
+#pragma unroll
+        for (int t = 0; t < TG; ++t)
+#pragma unroll
+          for (int j = 0; j < V; ++j) acc[t][j] = fmaf(xs[h][t], w[i][j], acc[t][j]);
       }
     }
   }
+  // rows within a warp by shuffles, then one line of sums a group of rows
+  const int cols = TG * EP;
 #pragma unroll
-  for (int t = 0; t < TG; ++t) red[t * kRouteThreads + tid] = acc[t];
-  __syncthreads();
-  float* part = a.logit_part + (size_t)(g * S + s) * TG * E;
-  for (int i = tid; i < TG * EP; i += kRouteThreads) {
-    const int t = i / EP, c = i % EP;
-    float v = 0.f;
-    for (int q = 0; q < R; ++q) v += red[t * kRouteThreads + q * EP + c];
-    if (c < E) part[t * E + c] = v;
+  for (int t = 0; t < TG; ++t)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float v = acc[t][j];
+      for (int o = CT; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      acc[t][j] = v;
+    }
+  const int lines = CT < 32 ? kRouteThreads / 32 : R;
+  const int line = CT < 32 ? warp : r;
+  if (CT >= 32 || lane < CT) {
+#pragma unroll
+    for (int t = 0; t < TG; ++t)
+#pragma unroll
+      for (int j = 0; j < V; ++j) red[line * cols + t * EP + c + j] = acc[t][j];
   }
+  __syncthreads();
+  float* part = a.logit_part + (size_t)(g * S + s) * cols;
+  for (int i = tid; i < cols; i += kRouteThreads) {
+    float v = 0.f;
+    for (int q = 0; q < lines; ++q) v += red[q * cols + i];
+    part[i] = v;
+  }
+  if (s == 0 && g == 0)
+    for (int i = tid; i < a.zero_ints; i += kRouteThreads) ((int*)a.cnt)[i] = 0;
   __threadfence();
   __syncthreads();
   if (tid == 0) {
@@ -85,65 +131,63 @@ decode_route_kernel(const Args a, int S, int EP) {
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // logits of this group's tokens: J threads a column, their sums in order
-  const float* all = a.logit_part + (size_t)g * S * TG * E;
-  const int C = TG * EP, J = C < kRouteThreads ? kRouteThreads / C : 1;
-  for (int c0 = 0; c0 < C; c0 += kRouteThreads / J) {
-    const int col = c0 + tid % (kRouteThreads / J), j = tid / (kRouteThreads / J);
-    const int t = col / EP, c = col % EP;
-    float v = 0.f;
-    if (c < E) {
+  // logits of this group's tokens: SL threads a vector of four columns over the
+  // slices, their sums in order
+  const float* all = a.logit_part + (size_t)g * S * cols;
+  const int CV = cols / 4, SL = kRouteThreads / CV;
+  {
+    const int cv = tid % CV, sl = tid / CV;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-      for (int q = j; q < S; q += J) v += __ldcg(all + (size_t)q * TG * E + t * E + c);
+    for (int q = sl; q < S; q += SL) {
+      const float4 o = __ldcg((const float4*)(all + (size_t)q * cols) + cv);
+      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
     }
-    red[c0 * J + tid] = v;            // [j][column] within this pass
+    ((float4*)red)[tid] = v;          // [sl][column]
   }
   __syncthreads();
-  if (J > 1) {
-    float v = 0.f;
-    if (tid < C)
-      for (int j = 0; j < J; ++j) v += red[j * C + tid];
-    __syncthreads();
-    if (tid < C) red[tid] = v;
+  if (SL > 1) {
+    for (int i = tid; i < cols; i += kRouteThreads) {
+      float v = 0.f;
+      for (int q = 0; q < SL; ++q) v += red[q * cols + i];
+      red[kRouteCols + i] = v;
+    }
     __syncthreads();
   }
-  const int warp = tid >> 5, lane = tid & 31;
   if (warp >= nt) return;
-  const float* lg = red + warp * EP;
-  float v[kMaxExperts / 32];
+  const float* lg = red + (SL > 1 ? kRouteCols : 0) + warp * EP;
+  // K rounds of arg-max over (value, id): the keys order totally and 0 marks
+  // one already taken, so the ids stay distinct
+  uint32_t key[kMaxExperts / 32];
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kMaxExperts / 32; ++i) {
-    const int c = i * 32 + lane;
-    v[i] = c < E && !isnan(lg[c]) ? lg[c] : -INFINITY;
-    m = fmaxf(m, v[i]);
+    const int e = i * 32 + lane;
+    key[i] = e < E ? order_key(lg[e]) : 0u;
+    if (e < E) m = fmaxf(m, lg[e]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  // K rounds of arg-max over (value, id); a NaN logit ranks like -infinity, so
-  // the order is total and the ids stay distinct
-  uint32_t taken = 0;
+  const int per = (E + 31) / 32;
   int my_id = 0;
-  float my_l = 0.f;
   for (int k = 0; k < a.K; ++k) {
-    float bv = -INFINITY;
-    int bi = kMaxExperts;
+    uint32_t best = 0u;
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-      const int c = i * 32 + lane;
-      if (c < E && !((taken >> i) & 1u) && (bi == kMaxExperts || v[i] > bv)) { bv = v[i]; bi = c; }
-    }
+    for (int i = 0; i < kMaxExperts / 32; ++i)
+      if (i < per) best = key[i] > best ? key[i] : best;
+    best = __reduce_max_sync(0xffffffffu, best);
+    uint32_t id = 0xffffffffu;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-      const bool better = oi < kMaxExperts && (bi == kMaxExperts || ov > bv || (!(bv > ov) && oi < bi));
-      if (better) { bv = ov; bi = oi; }
-    }
-    if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
-    if (lane == k) { my_id = bi; my_l = lg[bi]; }
+    for (int i = kMaxExperts / 32 - 1; i >= 0; --i)
+      if (i < per && key[i] == best) id = (uint32_t)(i * 32 + lane);
+    id = __reduce_min_sync(0xffffffffu, id);
+    const int at = (int)(id >> 5);
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i)
+      if (i == at && (int)(id & 31u) == lane) key[i] = 0u;
+    if (lane == k) my_id = (int)id;
   }
-  const float ek = lane < a.K ? expf(my_l - m) : 0.f;
+  const float ek = lane < a.K ? expf(lg[my_id] - m) : 0.f;
   const float Z = warp_sum(ek);
   if (lane < a.K) {
     const size_t at = (size_t)(t0 + warp) * a.K + lane;
@@ -266,6 +310,7 @@ decode_experts_kernel(const Args a) {
   const int tid = threadIdx.x;
   const T* x = (const T*)a.x;
   T* act = (T*)a.act;
+  clear_plan(sm.plan, kThreads);
   pdl_wait();
   build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
   const int slots = sm.plan.slots;
@@ -352,19 +397,19 @@ moe_status check(int N, int H, int E, int K, int F, moe_dtype dt) {
 }
 
 // The router's cut.  Tokens of a group share the reading of W_r; few tokens
-// take a group each, which leaves each block few values to add up at the end.
+// take a group each, which leaves the last block of a group little to add up.
 // Slices of H: enough blocks to fill the GPU twice over, of at least 64 rows.
 struct RouteCut {
   int TG, groups, S, EP;
 };
 RouteCut route_cut(int N, int H, int E) {
   RouteCut c;
-  c.TG = N <= 8 ? 1 : (N <= 16 ? 2 : (N <= 32 ? 4 : 8));
+  c.EP = 32;
+  while (c.EP < E) c.EP *= 2;
+  c.TG = N <= 8 ? 1 : (N <= 16 ? 2 : (N <= 32 || c.EP > kRouteCols / 8 ? 4 : 8));
   c.groups = (int)cdiv(N, c.TG);
   const int most = (int)cdiv(H, 64), want = (int)cdiv(296, c.groups);
   c.S = most < want ? most : want;
-  c.EP = 32;
-  while (c.EP < E) c.EP *= 2;
   return c;
 }
 
@@ -373,7 +418,7 @@ size_t part_bytes(int N, int H, int E) {
   size_t most = 0;
   for (int n = 1; n <= N; ++n) {
     const RouteCut c = route_cut(n, H, E);
-    const size_t b = (size_t)c.groups * c.S * c.TG * E * sizeof(float);
+    const size_t b = (size_t)c.groups * c.S * c.TG * c.EP * sizeof(float);
     if (b > most) most = b;
   }
   return most;
@@ -405,6 +450,7 @@ size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, 
   if (a) {
     a->status = (int*)base;
     a->arrive = (int*)(base + 64);
+    a->queue = (int*)(base + 192);
     a->cnt = (Counters*)cnt;
     a->zero_ints = (int)(zero / sizeof(int));
     w->tile_cnt = (int*)((char*)cnt + sizeof(Counters));
@@ -417,12 +463,13 @@ size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, 
   return off;
 }
 
-template <typename T>
-moe_status route(const Args& a, cudaStream_t s) {
-  const RouteCut c = route_cut(a.N, a.H, a.E);
+template <typename T, bool WIDE>
+void route(const Args& a, const RouteCut& c, cudaStream_t s) {
   const dim3 grid(c.S, c.groups);
-#define MOE_DECODE_ROUTE(G) \
-  case G: MOE_TRACED("decode_route", s, (decode_route_kernel<T, G><<<grid, kRouteThreads, 0, s>>>(a, c.S, c.EP))); break;
+#define MOE_DECODE_ROUTE(G)                                                                                   \
+  case G:                                                                                                     \
+    MOE_TRACED("decode_route", s, (decode_route_kernel<T, G, WIDE><<<grid, kRouteThreads, 0, s>>>(a, c.S, c.EP))); \
+    break;
   switch (c.TG) {
     MOE_DECODE_ROUTE(1)
     MOE_DECODE_ROUTE(2)
@@ -430,6 +477,13 @@ moe_status route(const Args& a, cudaStream_t s) {
     MOE_DECODE_ROUTE(8)
   }
 #undef MOE_DECODE_ROUTE
+}
+
+template <typename T>
+moe_status route_any(const Args& a, cudaStream_t s) {
+  const RouteCut c = route_cut(a.N, a.H, a.E);
+  if (a.E % Vec<T>::N == 0) route<T, true>(a, c, s);
+  else route<T, false>(a, c, s);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -498,7 +552,7 @@ moe_status moe_layer_decode(const void* x, const void* W_r, const void* W1, cons
   UmmaWs w;
   carve(&a, &w, (char*)ws, N, H, E, K, F, dt);
   cudaStream_t s = (cudaStream_t)stream;
-  const moe_status rs = dt == MOE_F32 ? route<float>(a, s) : route<__nv_bfloat16>(a, s);
+  const moe_status rs = dt == MOE_F32 ? route_any<float>(a, s) : route_any<__nv_bfloat16>(a, s);
   if (rs != MOE_OK) return rs;
   return dt == MOE_F32 ? experts<float>(a, s) : experts_umma(a, w.part_up, w.part_down, w.tile_cnt, s);
 }

@@ -13,12 +13,12 @@ namespace decode {
 constexpr int kMaxTokens = 128;
 constexpr int kMaxExperts = 256;
 constexpr int kMaskWords = kMaxTokens / 32;
-constexpr int kMaxGroups = 16;              // token groups of the router
+constexpr int kMaxGroups = 32;              // token groups of the router
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // Counters, zeroed by the router kernel of every call.
 struct Counters {
-  int ticket;                  // next unit of work
+  int ticket;                  // next unit of work (fp32)
   int abort;                   // a wait gave up: the others stop too
   int done_down;               // finished down-projection work, whole call
   int pad;
@@ -38,6 +38,7 @@ struct Args {
   // workspace
   int* status;
   int* arrive;                 // [kMaxGroups], inside the status region: zero between calls
+  int* queue;                  // bf16: next ticket and blocks that have left, zero between calls too
   Counters* cnt;
   int zero_ints;               // the router kernel zeroes this many from cnt on
   float* logit_part;           // [groups][S][TG][E]
@@ -63,9 +64,12 @@ struct Plan {
 };
 
 // All threads of a block of at least 256.
-__device__ __forceinline__ void build_plan(Plan& p, const int32_t* top, int N, int K, int E, int threads) {
+__device__ __forceinline__ void clear_plan(Plan& p, int threads) {
   for (int i = threadIdx.x; i < kMaxExperts * kMaskWords; i += threads) (&p.mask[0][0])[i] = 0;
   __syncthreads();
+}
+// After clear_plan, once the router has finished.
+__device__ __forceinline__ void build_plan(Plan& p, const int32_t* top, int N, int K, int E, int threads) {
   for (int i = threadIdx.x; i < N * K; i += threads) {
     const int e = __ldcg(top + i), n = i / K;
     if ((unsigned)e < (unsigned)E) atomicOr(&p.mask[e][n >> 5], 1u << (n & 31));

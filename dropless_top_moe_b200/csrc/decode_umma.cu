@@ -88,16 +88,14 @@ __device__ __forceinline__ Piece piece_at(const Line& l, int pos, int end) {
 __device__ __forceinline__ int entry_of(const Line& l, int t, int a) { return 2 * t + (t * l.q >= a ? 0 : 1); }
 
 struct Ticket {
-  bool up, sum, stop;
+  bool up, stop;
   int t;
 };
-__device__ __forceinline__ Ticket read_ticket(int v, const Line& up, const Line& down, int n_sum) {
+__device__ __forceinline__ Ticket read_ticket(int v, const Line& up, const Line& down) {
   Ticket k;
   k.up = v < up.tickets;
   k.t = k.up ? v : v - up.tickets;
-  k.sum = !k.up && k.t >= down.tickets;
-  if (k.sum) k.t -= down.tickets;
-  k.stop = k.sum && k.t >= n_sum;
+  k.stop = !k.up && k.t >= down.tickets;
   return k;
 }
 
@@ -132,9 +130,77 @@ struct Shared {
   int abort;
   int last;
   int ok;
+  float4 sum[kThreads];
 };
 
-constexpr int kVecSum = 4;     // columns of y a thread adds up
+// y[n] = sum_k w[n,k] out[row(n,k)], each out from its pieces in order.  Every
+// block takes its share of the columns; nothing waits for it.  KL threads share
+// the experts of four columns (thread kl those with k % KL = kl) and are added in
+// order; what does not depend on the down product is ready before the wait.
+__device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const Line& down) {
+  const Args& a = p.a;
+  const int tid = threadIdx.x;
+  const int per_row = a.H / 4, vecs = a.N * per_row;
+  const int KL = a.K > 4 ? 8 : (a.K > 2 ? 4 : a.K), VL = kThreads / KL;
+  const int vl = tid % VL, kl = tid / VL;
+  const int share = (vecs + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int v0 = (int)blockIdx.x * share, v1 = v0 + share < vecs ? v0 + share : vecs;
+  const size_t entry = (size_t)a.N * kPartFloats;
+  bool waited = false;
+  for (int vb = v0; vb < v1; vb += VL) {
+    const int at = vb + vl;
+    const bool in = at < v1;
+    const int n = in ? at / per_row : 0, h = in ? (at - n * per_row) * 4 : 0;
+    const int j = h >> 8;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = kl; i < a.K || !waited; i += KL) {
+      const bool mine = in && i < a.K;
+      float w = 0.f;
+      int row = 0, u = 0, a0 = 0, t0 = 0, t1 = 0;
+      if (mine) {
+        const int e = __ldcg(a.top + n * a.K + i);
+        w = __ldcg(a.weights + n * a.K + i);
+        u = sm.plan.slot_of[e];
+        row = plan_row(sm.plan, n, e);
+        a0 = (u * down.nj + j) * down.kc;
+        t0 = a0 / down.q;
+        t1 = (a0 + down.kc - 1) / down.q;
+      }
+      if (!waited) {
+        waited = true;
+        if (tid == 0) sm.ok = wait_count(&a.cnt->done_down, down.tickets, a.cnt, a.status);
+        __syncthreads();
+        if (!sm.ok) return;
+      }
+      if (!mine) break;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t0 == t1) {
+        o = __ldcg((const float4*)(a.out + (size_t)row * a.H + h));
+      } else {
+        const float* q0 = p.part_down + (size_t)((h >> 7) & 1) * a.N * 128 + (size_t)(row - sm.plan.off[u]) * 128 + (h & 127);
+#pragma unroll 4
+        for (int t = t0; t <= t1; ++t) {
+          const float4 q = __ldcg((const float4*)(q0 + entry * entry_of(down, t, a0)));
+          o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
+        }
+      }
+      s.x = fmaf(w, o.x, s.x); s.y = fmaf(w, o.y, s.y); s.z = fmaf(w, o.z, s.z); s.w = fmaf(w, o.w, s.w);
+    }
+    if (KL > 1) {
+      sm.sum[tid] = s;
+      __syncthreads();
+      if (kl == 0) {
+        for (int i = 1; i < KL; ++i) {
+          const float4 q = sm.sum[i * VL + vl];
+          s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (kl == 0 && in)
+      *(uint2*)((__nv_bfloat16*)a.y + (size_t)n * a.H + h) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
 decode_umma_kernel(const __grid_constant__ Params p) {
@@ -172,6 +238,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
     tmem_alloc(smem_u32(&sm.tmem), 512);
     tmem_relinquish();
   }
+  // tickets start at zero (the previous call's last block left them so), so the
+  // first one can be taken while the router still runs
+  int v = 0;
+  if (tid == 0) v = atomicAdd(a.queue, 1);
+  clear_plan(sm.plan, kThreads);
   pdl_wait();
   build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
   tc_fence_before();
@@ -180,8 +251,6 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   const uint32_t tmem = sm.tmem;
   const Line up = make_line(sm.plan.slots, a.F / 128, a.H / kKB);
   const Line down = make_line(sm.plan.slots, (a.H + 255) / 256, a.F / kKB);
-  const int vecs = a.N * (a.H / kVecSum);
-  const int n_sum = (vecs + 127) / 128;
 
   // the roles' view of the ticket ring
   int slot = 0;
@@ -196,8 +265,6 @@ decode_umma_kernel(const __grid_constant__ Params p) {
     uint32_t phase = 0;
     int64_t issued = 0;
     bool ok = true;
-    int v = 0;
-    if (lane == 0) v = atomicAdd(&a.cnt->ticket, 1);
     for (;;) {
       int next = 0;
       if (lane == 0) {
@@ -209,11 +276,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       if (!ok) break;
-      const Ticket k = read_ticket(__shfl_sync(0xffffffffu, v, 0), up, down, n_sum);
+      const Ticket k = read_ticket(__shfl_sync(0xffffffffu, v, 0), up, down);
       if (k.stop) break;
-      if (lane == 0) next = atomicAdd(&a.cnt->ticket, 1);     // arrives while this one's tiles are asked for
+      if (lane == 0) next = atomicAdd(a.queue, 1);     // arrives while this one's tiles are asked for
       next_slot();
-      if (!k.sum) {
+      {
         const Line& l = k.up ? up : down;
         const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
         for (int pos = k.t * l.q; pos < end && ok;) {
@@ -260,12 +327,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       if (lane == 0) ok = mbar_wait_bounded(bar(sm.ring_full[slot]), ring_phase, abort_flag, a.status, kTimeoutNs);
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       if (!ok) break;
-      const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down, n_sum);
+      const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.ring_empty[slot]));
       next_slot();
       if (k.stop) break;
-      if (k.sum) continue;
       const Line& l = k.up ? up : down;
       const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
       for (int pos = k.t * l.q; pos < end && ok;) {
@@ -328,12 +394,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       while (ok) {
         ok = mbar_wait_bounded(bar(sm.ring_full[slot]), ring_phase, abort_flag, a.status, kTimeoutNs);
         if (!ok) break;
-        const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down, n_sum);
+        const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down);
         mbar_arrive(bar(sm.ring_empty[slot]));
         next_slot();
         if (k.stop) break;
-        if (k.sum) continue;
-        const Line& l = k.up ? up : down;
+          const Line& l = k.up ? up : down;
         const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
         for (int pos = k.t * l.q; pos < end && ok;) {
           const Piece pc = piece_at(l, pos, end);
@@ -389,47 +454,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       if (lane == 0) ok = mbar_wait_bounded(bar(sm.ring_full[slot]), ring_phase, abort_flag, a.status, kTimeoutNs);
       ok = epi_all(ok);
       if (!ok) break;
-      const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down, n_sum);
+      const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.ring_empty[slot]));
       next_slot();
       if (k.stop) break;
-      if (k.sum) {
-        // y[n] = sum_k w[n,k] out[row(n,k)], k in order, each out from its pieces in order
-        if (lane == 0) {
-          ok = wait_count(&a.cnt->done_down, down.tickets, a.cnt, a.status);
-          if (!ok) *abort_flag = 1;
-        }
-        ok = epi_all(ok);
-        if (!ok) break;
-        const int at = k.t * 128 + et;
-        if (at < vecs) {
-          const int n = at / (a.H / kVecSum), h = (at - n * (a.H / kVecSum)) * kVecSum;
-          const int j = h >> 8;
-          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int i = 0; i < a.K; ++i) {
-            const int e = __ldcg(a.top + n * a.K + i);
-            const float w = __ldcg(a.weights + n * a.K + i);
-            const int u = sm.plan.slot_of[e], row = plan_row(sm.plan, n, e);
-            const int a0 = (u * down.nj + j) * down.kc;
-            const int t0 = a0 / down.q, t1 = (a0 + down.kc - 1) / down.q;
-            float4 o;
-            if (t0 == t1) {
-              o = __ldcg((const float4*)(a.out + (size_t)row * a.H + h));
-            } else {
-              const size_t in = (size_t)((h >> 7) & 1) * a.N * 128 + (size_t)(row - sm.plan.off[u]) * 128 + (h & 127);
-              o = make_float4(0.f, 0.f, 0.f, 0.f);
-              for (int t = t0; t <= t1; ++t) {
-                const float4 q = __ldcg((const float4*)(p.part_down + entry * entry_of(down, t, a0) + in));
-                o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
-              }
-            }
-            s.x = fmaf(w, o.x, s.x); s.y = fmaf(w, o.y, s.y); s.z = fmaf(w, o.z, s.z); s.w = fmaf(w, o.w, s.w);
-          }
-          *(uint2*)((__nv_bfloat16*)a.y + (size_t)n * a.H + h) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-        }
-        continue;
-      }
       const Line& l = k.up ? up : down;
       const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
       for (int pos = k.t * l.q; pos < end;) {
@@ -484,6 +513,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
               __threadfence();
               for (int c = 0; c < cnt; ++c) {
                 float g = 0.f, w = 0.f;
+#pragma unroll 4
                 for (int t = t0; t <= t1; ++t) {
                   const float* q = p.part_up + entry * entry_of(l, t, a0) + et;
                   g += __ldcg(q + (size_t)c * 128);
@@ -512,8 +542,16 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && sm.abort) *(volatile int*)&a.cnt->abort = 1;
   if (warp == 2) tmem_dealloc(tmem, 512);
+  if (!sm.abort) weighted_sums(p, sm, down);
+  __syncthreads();
+  if (tid == 0) {
+    if (sm.abort) *(volatile int*)&a.cnt->abort = 1;
+    if (atomicAdd(a.queue + 1, 1) == (int)gridDim.x - 1) {   // the last block out: ready for the next call
+      a.queue[0] = 0;
+      a.queue[1] = 0;
+    }
+  }
 }
 
 // ---- host --------------------------------------------------------------------
