@@ -26,20 +26,12 @@ namespace moe {
 namespace decode {
 namespace {
 
-constexpr int kRouteThreads = 256;
 constexpr int kRouteLoads = 8;       // rows of W_r a thread has in flight
-constexpr int kRouteCols = 1024;     // most (token, expert) sums of a block
-
-// Order of floats as unsigned numbers; NaN ranks like -infinity.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t b = __float_as_uint(isnan(v) ? -INFINITY : v);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
 
 // W_r columns: V neighbours a thread where E is a whole number of vectors, else one.
 template <typename T, int TG, bool WIDE>
 __global__ void __launch_bounds__(kRouteThreads)
-decode_route_kernel(const Args a, int S, int EP) {
+decode_route_kernel(const Args a, int S, int EP, int pick) {
   constexpr int V = WIDE ? Vec<T>::N : 1;
   __shared__ __align__(16) float xs[kRouteThreads * kRouteLoads / 8][TG];   // chunk rows x tokens
   __shared__ __align__(16) float red[8 * kRouteCols];
@@ -52,7 +44,8 @@ decode_route_kernel(const Args a, int S, int EP) {
   const int E = a.E, H = a.H;
   const int t0 = g * TG;
   const int nt = a.N - t0 < TG ? a.N - t0 : TG;
-  const int h0 = (int)((int64_t)H * s / S), h1 = (int)((int64_t)H * (s + 1) / S);
+  constexpr int XV = Vec<T>::N;                // slices and chunks are whole vectors of x
+  const int h0 = H / XV * s / S * XV, h1 = H / XV * (s + 1) / S * XV;
   const int CT = EP / V;                       // threads a row: a power of two
   const int R = kRouteThreads / CT;            // rows a pass
   const int c = (tid % CT) * V, r = tid / CT;
@@ -78,9 +71,12 @@ decode_route_kernel(const Args a, int S, int EP) {
       }
     }
     __syncthreads();
-    for (int i = tid; i < rows * TG; i += kRouteThreads) {
-      const int t = i / rows, h = i - t * rows;
-      xs[h][t] = t < nt ? to_f<T>(x[(size_t)(t0 + t) * H + c0 + h]) : 0.f;
+    for (int i = tid; i < rows / XV * TG; i += kRouteThreads) {
+      const int t = i % TG, h = i / TG * XV;
+      float f[XV];
+      Vec<T>::to_float(t < nt ? ld_nc_v4(x + (size_t)(t0 + t) * H + c0 + h) : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+      for (int j = 0; j < XV; ++j) xs[h + j][t] = f[j];
     }
     __syncthreads();
 #pragma unroll
@@ -122,6 +118,7 @@ decode_route_kernel(const Args a, int S, int EP) {
   }
   if (s == 0 && g == 0)
     for (int i = tid; i < a.zero_ints; i += kRouteThreads) ((int*)a.cnt)[i] = 0;
+  if (!pick) return;                  // the expert kernel goes on from here
   __threadfence();
   __syncthreads();
   if (tid == 0) {
@@ -131,69 +128,12 @@ decode_route_kernel(const Args a, int S, int EP) {
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // logits of this group's tokens: SL threads a vector of four columns over the
-  // slices, their sums in order
-  const float* all = a.logit_part + (size_t)g * S * cols;
-  const int CV = cols / 4, SL = kRouteThreads / CV;
-  {
-    const int cv = tid % CV, sl = tid / CV;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int q = sl; q < S; q += SL) {
-      const float4 o = __ldcg((const float4*)(all + (size_t)q * cols) + cv);
-      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-    }
-    ((float4*)red)[tid] = v;          // [sl][column]
-  }
-  __syncthreads();
-  if (SL > 1) {
-    for (int i = tid; i < cols; i += kRouteThreads) {
-      float v = 0.f;
-      for (int q = 0; q < SL; ++q) v += red[q * cols + i];
-      red[kRouteCols + i] = v;
-    }
-    __syncthreads();
-  }
-  if (warp >= nt) return;
-  const float* lg = red + (SL > 1 ? kRouteCols : 0) + warp * EP;
-  // K rounds of arg-max over (value, id): the keys order totally and 0 marks
-  // one already taken, so the ids stay distinct
-  uint32_t key[kMaxExperts / 32];
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kMaxExperts / 32; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = e < E ? order_key(lg[e]) : 0u;
-    if (e < E) m = fmaxf(m, lg[e]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const int per = (E + 31) / 32;
-  int my_id = 0;
-  for (int k = 0; k < a.K; ++k) {
-    uint32_t best = 0u;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-      if (i < per) best = key[i] > best ? key[i] : best;
-    best = __reduce_max_sync(0xffffffffu, best);
-    uint32_t id = 0xffffffffu;
-#pragma unroll
-    for (int i = kMaxExperts / 32 - 1; i >= 0; --i)
-      if (i < per && key[i] == best) id = (uint32_t)(i * 32 + lane);
-    id = __reduce_min_sync(0xffffffffu, id);
-    const int at = (int)(id >> 5);
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-      if (i == at && (int)(id & 31u) == lane) key[i] = 0u;
-    if (lane == k) my_id = (int)id;
-  }
-  const float ek = lane < a.K ? expf(lg[my_id] - m) : 0.f;
-  const float Z = warp_sum(ek);
-  if (lane < a.K) {
-    const size_t at = (size_t)(t0 + warp) * a.K + lane;
-    a.top[at] = my_id;
-    a.weights[at] = ek / Z;
-  }
+  pick_experts(a.logit_part + (size_t)g * S * cols, nt, EP, S, cols, EP, E, a.K, red,
+               [&](int t, int k, int e, float w) {
+                 const size_t at = (size_t)(t0 + t) * a.K + k;
+                 a.top[at] = e;
+                 a.weights[at] = w;
+               });
 }
 
 // ---- experts, one block of 256 threads a tile --------------------------------
@@ -399,9 +339,6 @@ moe_status check(int N, int H, int E, int K, int F, moe_dtype dt) {
 // The router's cut.  Tokens of a group share the reading of W_r; few tokens
 // take a group each, which leaves the last block of a group little to add up.
 // Slices of H: enough blocks to fill the GPU twice over, of at least 64 rows.
-struct RouteCut {
-  int TG, groups, S, EP;
-};
 RouteCut route_cut(int N, int H, int E) {
   RouteCut c;
   c.EP = 32;
@@ -464,11 +401,11 @@ size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, 
 }
 
 template <typename T, bool WIDE>
-void route(const Args& a, const RouteCut& c, cudaStream_t s) {
+void route(const Args& a, const RouteCut& c, int pick, cudaStream_t s) {
   const dim3 grid(c.S, c.groups);
 #define MOE_DECODE_ROUTE(G)                                                                                   \
   case G:                                                                                                     \
-    MOE_TRACED("decode_route", s, (decode_route_kernel<T, G, WIDE><<<grid, kRouteThreads, 0, s>>>(a, c.S, c.EP))); \
+    MOE_TRACED("decode_route", s, (decode_route_kernel<T, G, WIDE><<<grid, kRouteThreads, 0, s>>>(a, c.S, c.EP, pick))); \
     break;
   switch (c.TG) {
     MOE_DECODE_ROUTE(1)
@@ -480,10 +417,9 @@ void route(const Args& a, const RouteCut& c, cudaStream_t s) {
 }
 
 template <typename T>
-moe_status route_any(const Args& a, cudaStream_t s) {
-  const RouteCut c = route_cut(a.N, a.H, a.E);
-  if (a.E % Vec<T>::N == 0) route<T, true>(a, c, s);
-  else route<T, false>(a, c, s);
+moe_status route_any(const Args& a, const RouteCut& c, int pick, cudaStream_t s) {
+  if (a.E % Vec<T>::N == 0) route<T, true>(a, c, pick, s);
+  else route<T, false>(a, c, pick, s);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -552,9 +488,13 @@ moe_status moe_layer_decode(const void* x, const void* W_r, const void* W1, cons
   UmmaWs w;
   carve(&a, &w, (char*)ws, N, H, E, K, F, dt);
   cudaStream_t s = (cudaStream_t)stream;
-  const moe_status rs = dt == MOE_F32 ? route_any<float>(a, s) : route_any<__nv_bfloat16>(a, s);
-  if (rs != MOE_OK) return rs;
-  return dt == MOE_F32 ? experts<float>(a, s) : experts_umma(a, w.part_up, w.part_down, w.tile_cnt, s);
+  const RouteCut c = route_cut(N, H, E);
+  if (dt == MOE_F32) {
+    const moe_status rs = route_any<float>(a, c, 1, s);
+    return rs != MOE_OK ? rs : experts<float>(a, s);
+  }
+  const moe_status rs = route_any<__nv_bfloat16>(a, c, N > kPickTokens, s);
+  return rs != MOE_OK ? rs : experts_umma(a, c, w.part_up, w.part_down, w.tile_cnt, s);
 }
 
 }  // extern "C"

@@ -7,6 +7,8 @@
 #include "kernels.cuh"
 #include "umma.cuh"
 
+#include <math.h>
+
 namespace moe {
 namespace decode {
 
@@ -46,9 +48,100 @@ struct Args {
   float* out;                  // [N*K][H]
 };
 
+// ---- router ------------------------------------------------------------------
+// The router kernel leaves partial logits of slices of H, in groups of TG tokens:
+// logit_part[group][slice][token of the group][EP columns].
+constexpr int kRouteThreads = 256;
+constexpr int kRouteCols = 1024;     // most (token, expert) sums of a group
+// Up to this many tokens every block of the expert kernel picks the experts
+// itself from the partial logits, rather than wait for the router's last block to do it
+// and read the result: 2.6 us less of a 1-token call's 36 (2048/64/6/1408); with more
+// tokens the blocks would read more than they save.
+constexpr int kPickTokens = 8;
+struct RouteCut {
+  int TG, groups, S, EP;
+};
+
+// Order of floats as unsigned numbers; NaN ranks like -infinity.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(isnan(v) ? -INFINITY : v);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// kRouteThreads threads: the experts and weights of `rows` tokens, at most 8 and
+// at most kRouteCols / EP.  Slice q's partial logits of row r start at
+// all + r * row_stride + q * slice_stride; they are added in order.
+// put(row, k, id, weight).  red: 2 * kRouteCols floats.
+template <class Put>
+__device__ __forceinline__ void pick_experts(const float* all, int rows, size_t row_stride, int S,
+                                             size_t slice_stride, int EP, int E, int K, float* red, Put put) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int cols = EP;
+  while (cols < rows * EP) cols *= 2;
+  const int CV = cols / 4, SL = kRouteThreads / CV;       // SL threads add up four columns
+  {
+    const int cv = tid % CV, sl = tid / CV, r = cv * 4 / EP;
+    const float* at = all + r * row_stride + (cv * 4 - r * EP);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+#pragma unroll 8
+      for (int q = sl; q < S; q += SL) {
+        const float4 o = __ldcg((const float4*)(at + q * slice_stride));
+        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+      }
+    }
+    ((float4*)red)[tid] = v;          // [sl][column]
+  }
+  __syncthreads();
+  if (SL > 1) {
+    for (int i = tid; i < cols; i += kRouteThreads) {
+      float v = 0.f;
+      for (int q = 0; q < SL; ++q) v += red[q * cols + i];
+      red[kRouteCols + i] = v;
+    }
+    __syncthreads();
+  }
+  if (warp >= rows) return;
+  const float* lg = red + (SL > 1 ? kRouteCols : 0) + warp * EP;
+  // K rounds of arg-max over (value, id): the keys order totally and 0 marks
+  // one already taken, so the ids stay distinct
+  uint32_t key[kMaxExperts / 32];
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMaxExperts / 32; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e < E ? order_key(lg[e]) : 0u;
+    if (e < E) m = fmaxf(m, lg[e]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int per = (E + 31) / 32;
+  int my_id = 0;
+  for (int k = 0; k < K; ++k) {
+    uint32_t best = 0u;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i)
+      if (i < per) best = key[i] > best ? key[i] : best;
+    best = __reduce_max_sync(0xffffffffu, best);
+    uint32_t id = 0xffffffffu;
+#pragma unroll
+    for (int i = kMaxExperts / 32 - 1; i >= 0; --i)
+      if (i < per && key[i] == best) id = (uint32_t)(i * 32 + lane);
+    id = __reduce_min_sync(0xffffffffu, id);
+    const int at = (int)(id >> 5);
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i)
+      if (i == at && (int)(id & 31u) == lane) key[i] = 0u;
+    if (lane == k) my_id = (int)id;
+  }
+  const float ek = lane < K ? expf(lg[my_id] - m) : 0.f;
+  const float Z = warp_sum(ek);
+  if (lane < K) put(warp, lane, my_id, ek / Z);
+}
+
 // decode_umma.cu: the expert kernel for bf16
 size_t umma_part_bytes(int N);   // partial sums of one phase
-moe_status experts_umma(const Args& a, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s);
+moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s);
 
 // ---- plan: which experts are used, by which tokens ---------------------------
 // Slots are the used experts in increasing id; a slot's rows are its tokens in
@@ -68,12 +161,15 @@ __device__ __forceinline__ void clear_plan(Plan& p, int threads) {
   for (int i = threadIdx.x; i < kMaxExperts * kMaskWords; i += threads) (&p.mask[0][0])[i] = 0;
   __syncthreads();
 }
-// After clear_plan, once the router has finished.
+__device__ __forceinline__ void plan_add(Plan& p, int n, int e) { atomicOr(&p.mask[e][n >> 5], 1u << (n & 31)); }
+// After clear_plan, once the ids are there: from the router's output, or (top
+// NULL) added with plan_add.
 __device__ __forceinline__ void build_plan(Plan& p, const int32_t* top, int N, int K, int E, int threads) {
-  for (int i = threadIdx.x; i < N * K; i += threads) {
-    const int e = __ldcg(top + i), n = i / K;
-    if ((unsigned)e < (unsigned)E) atomicOr(&p.mask[e][n >> 5], 1u << (n & 31));
-  }
+  if (top)
+    for (int i = threadIdx.x; i < N * K; i += threads) {
+      const int e = __ldcg(top + i);
+      if ((unsigned)e < (unsigned)E) plan_add(p, i / K, e);
+    }
   __syncthreads();
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   int rows = 0, urows = 0, uslots = 0;

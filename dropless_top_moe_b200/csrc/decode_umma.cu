@@ -53,6 +53,7 @@ struct Params {
   float* part_up;              // [2 * tickets][2][N][128]
   float* part_down;
   int* tile_cnt;               // [slots][F / 128] pieces that have arrived, zeroed by the router
+  RouteCut cut;
   int stages;
   int b_bytes;                 // of a stage: N rounded up to 16 rows of 128 bytes
 };
@@ -131,60 +132,70 @@ struct Shared {
   int last;
   int ok;
   float4 sum[kThreads];
+  int pick_id[kPickTokens][32];
+  float pick_w[kPickTokens][32];
+  // of the one or two tokens whose columns this block adds up
+  float w[2][32];
+  int row[2][32], tile[2][32], row0[2][32];
 };
+static_assert(kMaxTokens <= kBlocks, "a block's share of y is at most a row, so it lies in two");
+static_assert(kThreads == kRouteThreads, "pick_experts");
 
 // y[n] = sum_k w[n,k] out[row(n,k)], each out from its pieces in order.  Every
-// block takes its share of the columns; nothing waits for it.  KL threads share
-// the experts of four columns (thread kl those with k % KL = kl) and are added in
-// order; what does not depend on the down product is ready before the wait.
+// block takes its share of the columns; nothing waits for it.  What does not
+// depend on the down product is ready before the wait.  KL threads share the
+// experts of four columns (thread kl those with k % KL = kl) and are added in
+// order, KL as large as the share leaves threads for: with few columns a block the
+// time is one chain of loads.
 __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const Line& down) {
   const Args& a = p.a;
   const int tid = threadIdx.x;
   const int per_row = a.H / 4, vecs = a.N * per_row;
-  const int KL = a.K > 4 ? 8 : (a.K > 2 ? 4 : a.K), VL = kThreads / KL;
-  const int vl = tid % VL, kl = tid / VL;
-  const int share = (vecs + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int share = (vecs + kBlocks - 1) / kBlocks;
   const int v0 = (int)blockIdx.x * share, v1 = v0 + share < vecs ? v0 + share : vecs;
+  if (v0 >= v1) return;
+  int KL = 1;
+  while (KL < 8 && KL < a.K && 2 * KL * share <= kThreads) KL *= 2;
+  const int VL = kThreads / KL, vl = tid % VL, kl = tid / VL;
+  const int first = v0 / per_row;
+  if (tid < 2 * a.K) {
+    const int i = tid / a.K, k = tid - i * a.K, n = first + i;
+    if (n < a.N) {
+      const bool here = a.N <= kPickTokens;
+      const int e = here ? sm.pick_id[n][k] : __ldcg(a.top + n * a.K + k);
+      const int u = sm.plan.slot_of[e];
+      sm.w[i][k] = here ? sm.pick_w[n][k] : __ldcg(a.weights + n * a.K + k);
+      sm.row[i][k] = plan_row(sm.plan, n, e);
+      sm.row0[i][k] = sm.plan.off[u];
+      sm.tile[i][k] = u * down.nj;
+    }
+  }
+  if (tid == 0) sm.ok = wait_count(&a.cnt->done_down, down.tickets, a.cnt, a.status);
+  __syncthreads();
+  if (!sm.ok) return;
   const size_t entry = (size_t)a.N * kPartFloats;
-  bool waited = false;
   for (int vb = v0; vb < v1; vb += VL) {
     const int at = vb + vl;
     const bool in = at < v1;
-    const int n = in ? at / per_row : 0, h = in ? (at - n * per_row) * 4 : 0;
-    const int j = h >> 8;
+    const int n = in ? at / per_row : first, h = in ? (at - n * per_row) * 4 : 0;
+    const int ti = n - first, j = h >> 8;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = kl; i < a.K || !waited; i += KL) {
-      const bool mine = in && i < a.K;
-      float w = 0.f;
-      int row = 0, u = 0, a0 = 0, t0 = 0, t1 = 0;
-      if (mine) {
-        const int e = __ldcg(a.top + n * a.K + i);
-        w = __ldcg(a.weights + n * a.K + i);
-        u = sm.plan.slot_of[e];
-        row = plan_row(sm.plan, n, e);
-        a0 = (u * down.nj + j) * down.kc;
-        t0 = a0 / down.q;
-        t1 = (a0 + down.kc - 1) / down.q;
-      }
-      if (!waited) {
-        waited = true;
-        if (tid == 0) sm.ok = wait_count(&a.cnt->done_down, down.tickets, a.cnt, a.status);
-        __syncthreads();
-        if (!sm.ok) return;
-      }
-      if (!mine) break;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t0 == t1) {
-        o = __ldcg((const float4*)(a.out + (size_t)row * a.H + h));
-      } else {
-        const float* q0 = p.part_down + (size_t)((h >> 7) & 1) * a.N * 128 + (size_t)(row - sm.plan.off[u]) * 128 + (h & 127);
+    if (in) {
 #pragma unroll 4
-        for (int t = t0; t <= t1; ++t) {
-          const float4 q = __ldcg((const float4*)(q0 + entry * entry_of(down, t, a0)));
+      for (int k = kl; k < a.K; k += KL) {
+        const float w = sm.w[ti][k];
+        const int row = sm.row[ti][k];
+        const int a0 = (sm.tile[ti][k] + j) * down.kc;
+        const int t0 = a0 / down.q, t1 = (a0 + down.kc - 1) / down.q;
+        const float* q0 = p.part_down + (size_t)((h >> 7) & 1) * a.N * 128 +
+                          (size_t)(row - sm.row0[ti][k]) * 128 + (h & 127);
+        float4 o = __ldcg((const float4*)(t0 == t1 ? a.out + (size_t)row * a.H + h : q0 + entry * entry_of(down, t0, a0)));
+        for (int t = t0 + 1; t <= t1; ++t) {
+          const float4 q = __ldcg((const float4*)(q0 + entry * (2 * t)));
           o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
         }
+        s.x = fmaf(w, o.x, s.x); s.y = fmaf(w, o.y, s.y); s.z = fmaf(w, o.z, s.z); s.w = fmaf(w, o.w, s.w);
       }
-      s.x = fmaf(w, o.x, s.x); s.y = fmaf(w, o.y, s.y); s.z = fmaf(w, o.z, s.z); s.w = fmaf(w, o.w, s.w);
     }
     if (KL > 1) {
       sm.sum[tid] = s;
@@ -244,7 +255,29 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   if (tid == 0) v = atomicAdd(a.queue, 1);
   clear_plan(sm.plan, kThreads);
   pdl_wait();
-  build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
+  if (a.N <= kPickTokens) {
+    const int EP = p.cut.EP, S = p.cut.S, K = a.K;     // groups of one token
+    const int pass = kRouteCols / EP < kPickTokens ? kRouteCols / EP : kPickTokens;
+    float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));   // the ring is still empty
+    for (int n0 = 0; n0 < a.N; n0 += pass) {
+      if (n0) __syncthreads();
+      pick_experts(a.logit_part + (size_t)n0 * S * EP, a.N - n0 < pass ? a.N - n0 : pass, (size_t)S * EP, S, EP, EP,
+                   a.E, K, red, [&](int r, int k, int e, float w) {
+                     const int n = n0 + r;
+                     plan_add(sm.plan, n, e);
+                     sm.pick_id[n][k] = e;
+                     sm.pick_w[n][k] = w;
+                     if (blockIdx.x == 0) {
+                       a.top[n * K + k] = e;
+                       a.weights[n * K + k] = w;
+                     }
+                   });
+    }
+    build_plan(sm.plan, nullptr, a.N, K, a.E, kThreads);
+    fence_proxy_async();       // `red` was written where TMA will write
+  } else {
+    build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -266,7 +299,6 @@ decode_umma_kernel(const __grid_constant__ Params p) {
     int64_t issued = 0;
     bool ok = true;
     for (;;) {
-      int next = 0;
       if (lane == 0) {
         ok = mbar_wait_bounded(bar(sm.ring_empty[slot]), ring_phase ^ 1u, abort_flag, a.status, kTimeoutNs);
         if (ok) {
@@ -278,7 +310,6 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       if (!ok) break;
       const Ticket k = read_ticket(__shfl_sync(0xffffffffu, v, 0), up, down);
       if (k.stop) break;
-      if (lane == 0) next = atomicAdd(a.queue, 1);     // arrives while this one's tiles are asked for
       next_slot();
       {
         const Line& l = k.up ? up : down;
@@ -306,7 +337,9 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         }
       }
       if (!ok) break;
-      v = next;
+      // not earlier: a block that runs ahead of the others would take work that
+      // it can only queue, and the ring hides the round trip
+      if (lane == 0) v = atomicAdd(a.queue, 1);
     }
     if (lane == 0) {
       // the copies in flight land before the block leaves, also after a wait gave up
@@ -588,10 +621,11 @@ bool map3(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2
 
 size_t umma_part_bytes(int N) { return (size_t)(2 * 2 * kBlocks) * N * kPartFloats * sizeof(float); }
 
-moe_status experts_umma(const Args& a, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s) {
+moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s) {
   Params p;
   memset(&p, 0, sizeof(p));
   p.a = a;
+  p.cut = cut;
   p.part_up = part_up;
   p.part_down = part_down;
   p.tile_cnt = tile_cnt;
