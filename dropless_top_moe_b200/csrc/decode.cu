@@ -26,15 +26,59 @@ namespace moe {
 namespace decode {
 namespace {
 
-constexpr int kRouteLoads = 8;       // rows of W_r a thread has in flight
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteLoads = 16;      // rows of W_r a thread has in flight
+constexpr int kRouteRows = kRouteWarps * kRouteLoads;
 
-// W_r columns: V neighbours a thread where E is a whole number of vectors, else one.
-template <typename T, int TG, bool WIDE>
+// V neighbouring elements of a row, as they lie in memory.
+template <typename T, int V>
+struct Raw {
+  static constexpr int B = V * (int)sizeof(T), W = B < 4 ? 1 : B / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const T* p) {      // p aligned to B (16 at most)
+    if constexpr (B >= 16) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 v = __ldg((const uint4*)p + i / 4);
+        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+      }
+    } else if constexpr (B == 8) {
+      const uint2 v = __ldg((const uint2*)p);
+      w[0] = v.x; w[1] = v.y;
+    } else if constexpr (B == 4) {
+      w[0] = __ldg((const uint32_t*)p);
+    } else {
+      w[0] = __ldg((const uint16_t*)p);
+    }
+  }
+  __device__ __forceinline__ void load_each(const T* p, int n) {   // the first n elements, one by one
+    zero();
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < n) {
+        if constexpr (sizeof(T) == 4) w[j] = __ldg((const uint32_t*)p + j);
+        else w[j / 2] |= (uint32_t)__ldg((const uint16_t*)p + j) << (16 * (j & 1));
+      }
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    else return j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+  }
+};
+
+// A warp takes a row of W_r at a time, V = EP / 32 neighbouring columns a lane, so
+// nothing is added across lanes; `wide`: E is a whole number of V columns and a
+// lane's are one load.
+template <typename T, int TG, int V>
 __global__ void __launch_bounds__(kRouteThreads)
-decode_route_kernel(const Args a, int S, int EP, int pick) {
-  constexpr int V = WIDE ? Vec<T>::N : 1;
-  __shared__ __align__(16) float xs[kRouteThreads * kRouteLoads / 8][TG];   // chunk rows x tokens
-  __shared__ __align__(16) float red[8 * kRouteCols];
+decode_route_kernel(const Args a, int S, int wide, int pick) {
+  constexpr int EP = 32 * V, cols = TG * EP;
+  __shared__ __align__(16) float xs[kRouteRows][TG];
+  __shared__ __align__(16) float red[kRouteWarps * cols > 2 * kRouteCols ? kRouteWarps * cols : 2 * kRouteCols];
   __shared__ int last;
   pdl_launch();
   const int tid = threadIdx.x, g = blockIdx.y, s = blockIdx.x;
@@ -44,31 +88,29 @@ decode_route_kernel(const Args a, int S, int EP, int pick) {
   const int E = a.E, H = a.H;
   const int t0 = g * TG;
   const int nt = a.N - t0 < TG ? a.N - t0 : TG;
-  constexpr int XV = Vec<T>::N;                // slices and chunks are whole vectors of x
+  constexpr int XV = Vec<T>::N;                // slices are whole vectors of x
   const int h0 = H / XV * s / S * XV, h1 = H / XV * (s + 1) / S * XV;
-  const int CT = EP / V;                       // threads a row: a power of two
-  const int R = kRouteThreads / CT;            // rows a pass
-  const int c = (tid % CT) * V, r = tid / CT;
-  const int chunk = R * kRouteLoads < (int)(sizeof(xs) / sizeof(xs[0])) ? R * kRouteLoads : (int)(sizeof(xs) / sizeof(xs[0]));
+  const int c = lane * V;
   float acc[TG][V];
 #pragma unroll
   for (int t = 0; t < TG; ++t)
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[t][j] = 0.f;
-  for (int c0 = h0; c0 < h1; c0 += chunk) {
-    const int rows = h1 - c0 < chunk ? h1 - c0 : chunk;
+  for (int c0 = h0; c0 < h1; c0 += kRouteRows) {
+    const int rows = h1 - c0 < kRouteRows ? h1 - c0 : kRouteRows;
     // the weights' loads go out before x is staged
-    float w[kRouteLoads][V];
-    uint4 wv[kRouteLoads];
+    Raw<T, V> w[kRouteLoads];
+    const T* at = wr + (size_t)(c0 + warp) * E + c;
+    if (wide) {
 #pragma unroll
-    for (int i = 0; i < kRouteLoads; ++i) {
-      const int h = r + i * R;
-      const bool in = h < rows && c < E;
-      if (WIDE) {
-        wv[i] = in ? ld_nc_v4(wr + (size_t)(c0 + h) * E + c) : make_uint4(0, 0, 0, 0);
-      } else {
-        w[i][0] = in ? to_f<T>(wr[(size_t)(c0 + h) * E + c]) : 0.f;
+      for (int i = 0; i < kRouteLoads; ++i) {
+        w[i].zero();
+        if (warp + i * kRouteWarps < rows && c < E) w[i].load(at + (size_t)i * kRouteWarps * E);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRouteLoads; ++i)
+        w[i].load_each(at + (size_t)i * kRouteWarps * E, warp + i * kRouteWarps < rows ? E - c : 0);
     }
     __syncthreads();
     for (int i = tid; i < rows / XV * TG; i += kRouteThreads) {
@@ -81,39 +123,25 @@ decode_route_kernel(const Args a, int S, int EP, int pick) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kRouteLoads; ++i) {
-      const int h = r + i * R;
+      const int h = warp + i * kRouteWarps;
       if (h < rows) {
-        if constexpr (WIDE) Vec<T>::to_float(wv[i], w[i]);
 #pragma unroll
         for (int t = 0; t < TG; ++t)
 #pragma unroll
-          for (int j = 0; j < V; ++j) acc[t][j] = fmaf(xs[h][t], w[i][j], acc[t][j]);
+          for (int j = 0; j < V; ++j) acc[t][j] = fmaf(xs[h][t], w[i].at(j), acc[t][j]);
       }
     }
   }
-  // rows within a warp by shuffles, then one line of sums a group of rows
-  const int cols = TG * EP;
 #pragma unroll
   for (int t = 0; t < TG; ++t)
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float v = acc[t][j];
-      for (int o = CT; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      acc[t][j] = v;
-    }
-  const int lines = CT < 32 ? kRouteThreads / 32 : R;
-  const int line = CT < 32 ? warp : r;
-  if (CT >= 32 || lane < CT) {
-#pragma unroll
-    for (int t = 0; t < TG; ++t)
-#pragma unroll
-      for (int j = 0; j < V; ++j) red[line * cols + t * EP + c + j] = acc[t][j];
-  }
+    for (int j = 0; j < V; ++j) red[warp * cols + t * EP + c + j] = acc[t][j];
   __syncthreads();
   float* part = a.logit_part + (size_t)(g * S + s) * cols;
   for (int i = tid; i < cols; i += kRouteThreads) {
     float v = 0.f;
-    for (int q = 0; q < lines; ++q) v += red[q * cols + i];
+#pragma unroll
+    for (int q = 0; q < kRouteWarps; ++q) v += red[q * cols + i];
     part[i] = v;
   }
   if (s == 0 && g == 0)
@@ -128,8 +156,8 @@ decode_route_kernel(const Args a, int S, int EP, int pick) {
   __syncthreads();
   if (!last) return;
   __threadfence();
-  pick_experts(a.logit_part + (size_t)g * S * cols, nt, EP, S, cols, EP, E, a.K, red,
-               [&](int t, int k, int e, float w) {
+  pick_experts<V>(a.logit_part + (size_t)g * S * cols, nt, EP, S, cols, E, a.K, red,
+                  [&](int t, int k, int e, float w) {
                  const size_t at = (size_t)(t0 + t) * a.K + k;
                  a.top[at] = e;
                  a.weights[at] = w;
@@ -343,7 +371,7 @@ RouteCut route_cut(int N, int H, int E) {
   RouteCut c;
   c.EP = 32;
   while (c.EP < E) c.EP *= 2;
-  c.TG = N <= 8 ? 1 : (N <= 16 ? 2 : (N <= 32 || c.EP > kRouteCols / 8 ? 4 : 8));
+  c.TG = N <= 8 ? 1 : (N <= 32 ? 2 : 4);
   c.groups = (int)cdiv(N, c.TG);
   const int most = (int)cdiv(H, 64), want = (int)cdiv(296, c.groups);
   c.S = most < want ? most : want;
@@ -400,14 +428,16 @@ size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, 
   return off;
 }
 
-template <typename T, bool WIDE>
+template <typename T, int TG>
 void route(const Args& a, const RouteCut& c, int pick, cudaStream_t s) {
   const dim3 grid(c.S, c.groups);
-#define MOE_DECODE_ROUTE(G)                                                                                   \
-  case G:                                                                                                     \
-    MOE_TRACED("decode_route", s, (decode_route_kernel<T, G, WIDE><<<grid, kRouteThreads, 0, s>>>(a, c.S, c.EP, pick))); \
+  const int wide = a.E % (c.EP / 32) == 0;
+#define MOE_DECODE_ROUTE(V)                                                                                    \
+  case 32 * V:                                                                                                 \
+    MOE_TRACED("decode_route", s,                                                                              \
+               (decode_route_kernel<T, TG, V><<<grid, kRouteThreads, 0, s>>>(a, c.S, wide, pick)));            \
     break;
-  switch (c.TG) {
+  switch (c.EP) {
     MOE_DECODE_ROUTE(1)
     MOE_DECODE_ROUTE(2)
     MOE_DECODE_ROUTE(4)
@@ -418,8 +448,9 @@ void route(const Args& a, const RouteCut& c, int pick, cudaStream_t s) {
 
 template <typename T>
 moe_status route_any(const Args& a, const RouteCut& c, int pick, cudaStream_t s) {
-  if (a.E % Vec<T>::N == 0) route<T, true>(a, c, pick, s);
-  else route<T, false>(a, c, pick, s);
+  if (c.TG == 1) route<T, 1>(a, c, pick, s);
+  else if (c.TG == 2) route<T, 2>(a, c, pick, s);
+  else route<T, 4>(a, c, pick, s);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

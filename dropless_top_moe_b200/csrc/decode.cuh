@@ -57,7 +57,7 @@ constexpr int kRouteCols = 1024;     // most (token, expert) sums of a group
 // itself from the partial logits, rather than wait for the router's last block to do it
 // and read the result: 2.6 us less of a 1-token call's 36 (2048/64/6/1408); with more
 // tokens the blocks would read more than they save.
-constexpr int kPickTokens = 8;
+constexpr int kPickTokens = 2;
 struct RouteCut {
   int TG, groups, S, EP;
 };
@@ -69,69 +69,76 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 
 // kRouteThreads threads: the experts and weights of `rows` tokens, at most 8 and
-// at most kRouteCols / EP.  Slice q's partial logits of row r start at
+// at most kRouteCols / EP, EP = 32 V.  Slice q's partial logits of row r start at
 // all + r * row_stride + q * slice_stride; they are added in order.
 // put(row, k, id, weight).  red: 2 * kRouteCols floats.
-template <class Put>
+template <int V, class Put>
 __device__ __forceinline__ void pick_experts(const float* all, int rows, size_t row_stride, int S,
-                                             size_t slice_stride, int EP, int E, int K, float* red, Put put) {
+                                             size_t slice_stride, int E, int K, float* red, Put put) {
+  constexpr int EP = 32 * V, QV = EP / 4;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int cols = EP;
-  while (cols < rows * EP) cols *= 2;
-  const int CV = cols / 4, SL = kRouteThreads / CV;       // SL threads add up four columns
+  int lc = __ffs(QV) - 1;                     // log2 of the vectors of all rows
+  while ((1 << lc) < rows * QV) ++lc;
+  const int CV = 1 << lc, SL = kRouteThreads >> lc, cols = CV * 4;   // SL threads add up four columns
   {
-    const int cv = tid % CV, sl = tid / CV, r = cv * 4 / EP;
-    const float* at = all + r * row_stride + (cv * 4 - r * EP);
+    const int cv = tid & (CV - 1), sl = tid >> lc, r = cv / QV;
+    const float* at = all + r * row_stride + (cv % QV) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < rows) {
-#pragma unroll 8
-      for (int q = sl; q < S; q += SL) {
-        const float4 o = __ldcg((const float4*)(at + q * slice_stride));
-        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+      for (int q = sl; q < S; q += 8 * SL) {        // eight slices in flight
+        float4 o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          o[i] = q + i * SL < S ? __ldcg((const float4*)(at + (q + i * SL) * slice_stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) { v.x += o[i].x; v.y += o[i].y; v.z += o[i].z; v.w += o[i].w; }
       }
     }
-    ((float4*)red)[tid] = v;          // [sl][column]
-  }
-  __syncthreads();
-  if (SL > 1) {
+    for (int o = CV; o < 32; o <<= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+      v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+    }
+    const int lines = CV < 32 ? kRouteThreads / 32 : SL;
+    if (CV >= 32 || lane < CV) ((float4*)red)[(CV < 32 ? warp : sl) * CV + cv] = v;
+    __syncthreads();
     for (int i = tid; i < cols; i += kRouteThreads) {
-      float v = 0.f;
-      for (int q = 0; q < SL; ++q) v += red[q * cols + i];
-      red[kRouteCols + i] = v;
+      float t = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) t += q < lines ? red[q * cols + i] : 0.f;
+      red[kRouteCols + i] = t;
     }
     __syncthreads();
   }
   if (warp >= rows) return;
-  const float* lg = red + (SL > 1 ? kRouteCols : 0) + warp * EP;
+  const float* lg = red + kRouteCols + warp * EP;
   // K rounds of arg-max over (value, id): the keys order totally and 0 marks
   // one already taken, so the ids stay distinct
-  uint32_t key[kMaxExperts / 32];
+  uint32_t key[V];
   float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kMaxExperts / 32; ++i) {
+  for (int i = 0; i < V; ++i) {
     const int e = i * 32 + lane;
     key[i] = e < E ? order_key(lg[e]) : 0u;
     if (e < E) m = fmaxf(m, lg[e]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const int per = (E + 31) / 32;
   int my_id = 0;
   for (int k = 0; k < K; ++k) {
-    uint32_t best = 0u;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-      if (i < per) best = key[i] > best ? key[i] : best;
+    for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
     best = __reduce_max_sync(0xffffffffu, best);
     uint32_t id = 0xffffffffu;
 #pragma unroll
-    for (int i = kMaxExperts / 32 - 1; i >= 0; --i)
-      if (i < per && key[i] == best) id = (uint32_t)(i * 32 + lane);
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] == best) id = (uint32_t)(i * 32 + lane);
     id = __reduce_min_sync(0xffffffffu, id);
-    const int at = (int)(id >> 5);
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-      if (i == at && (int)(id & 31u) == lane) key[i] = 0u;
+    for (int i = 0; i < V; ++i)
+      if (id == (uint32_t)(i * 32 + lane)) key[i] = 0u;
     if (lane == k) my_id = (int)id;
   }
   const float ek = lane < K ? expf(lg[my_id] - m) : 0.f;

@@ -42,6 +42,7 @@ constexpr int kKB = 64;                     // rows of a unit
 constexpr int kABytes = 4 * 8192;           // four 64 x 64 weight boxes
 constexpr int kMaxStages = 6;
 constexpr int kRing = 8;                    // tickets in flight in a block
+constexpr int kPrefetchUnits = 32;          // longest down ticket whose rest is prefetched
 constexpr int kSmemData = 210 * 1024;
 constexpr int kPartFloats = 2 * 128;        // a token's sums of one piece
 
@@ -189,10 +190,15 @@ __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const
         const int t0 = a0 / down.q, t1 = (a0 + down.kc - 1) / down.q;
         const float* q0 = p.part_down + (size_t)((h >> 7) & 1) * a.N * 128 +
                           (size_t)(row - sm.row0[ti][k]) * 128 + (h & 127);
-        float4 o = __ldcg((const float4*)(t0 == t1 ? a.out + (size_t)row * a.H + h : q0 + entry * entry_of(down, t0, a0)));
-        for (int t = t0 + 1; t <= t1; ++t) {
-          const float4 q = __ldcg((const float4*)(q0 + entry * (2 * t)));
-          o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
+        const float* at0 = t0 == t1 ? a.out + (size_t)row * a.H + h : q0 + entry * entry_of(down, t0, a0);
+        float4 o = __ldcg((const float4*)at0);
+        for (int t = t0 + 1; t <= t1; t += 3) {      // three pieces in flight
+          float4 q[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            q[i] = t + i <= t1 ? __ldcg((const float4*)(q0 + entry * (2 * (t + i)))) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) { o.x += q[i].x; o.y += q[i].y; o.z += q[i].z; o.w += q[i].w; }
         }
         s.x = fmaf(w, o.x, s.x); s.y = fmaf(w, o.y, s.y); s.z = fmaf(w, o.z, s.z); s.w = fmaf(w, o.w, s.w);
       }
@@ -211,6 +217,23 @@ __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const
     if (kl == 0 && in)
       *(uint2*)((__nv_bfloat16*)a.y + (size_t)n * a.H + h) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
+}
+
+// The experts of up to kPickTokens tokens, from the router's groups of one token.
+template <int V>
+__device__ __forceinline__ void pick_here(const Params& p, Shared& sm, float* red) {
+  static_assert(kPickTokens * 32 * V <= kRouteCols, "one pass");
+  const Args& a = p.a;
+  const int S = p.cut.S, EP = 32 * V;
+  pick_experts<V>(a.logit_part, a.N, (size_t)S * EP, S, EP, a.E, a.K, red, [&](int n, int k, int e, float w) {
+    plan_add(sm.plan, n, e);
+    sm.pick_id[n][k] = e;
+    sm.pick_w[n][k] = w;
+    if (blockIdx.x == 0) {
+      a.top[n * a.K + k] = e;
+      a.weights[n * a.K + k] = w;
+    }
+  });
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -256,24 +279,14 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   clear_plan(sm.plan, kThreads);
   pdl_wait();
   if (a.N <= kPickTokens) {
-    const int EP = p.cut.EP, S = p.cut.S, K = a.K;     // groups of one token
-    const int pass = kRouteCols / EP < kPickTokens ? kRouteCols / EP : kPickTokens;
     float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));   // the ring is still empty
-    for (int n0 = 0; n0 < a.N; n0 += pass) {
-      if (n0) __syncthreads();
-      pick_experts(a.logit_part + (size_t)n0 * S * EP, a.N - n0 < pass ? a.N - n0 : pass, (size_t)S * EP, S, EP, EP,
-                   a.E, K, red, [&](int r, int k, int e, float w) {
-                     const int n = n0 + r;
-                     plan_add(sm.plan, n, e);
-                     sm.pick_id[n][k] = e;
-                     sm.pick_w[n][k] = w;
-                     if (blockIdx.x == 0) {
-                       a.top[n * K + k] = e;
-                       a.weights[n * K + k] = w;
-                     }
-                   });
+    switch (p.cut.EP) {
+      case 32: pick_here<1>(p, sm, red); break;
+      case 64: pick_here<2>(p, sm, red); break;
+      case 128: pick_here<4>(p, sm, red); break;
+      default: pick_here<8>(p, sm, red); break;
     }
-    build_plan(sm.plan, nullptr, a.N, K, a.E, kThreads);
+    build_plan(sm.plan, nullptr, a.N, a.K, a.E, kThreads);
     fence_proxy_async();       // `red` was written where TMA will write
   } else {
     build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
@@ -321,6 +334,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           // lane 0-3: one 64-column box each
           const CUtensorMap* m = !k.up ? &p.tw2 : (lane < 2 ? &p.tw1 : &p.tw3);
           const int c = k.up ? j * 128 + (lane & 1) * 64 : j * 256 + lane * 64;
+          // the activations these meet may be some time yet: what the ring cannot
+          // hold of a short ticket waits in L2
+          if (!k.up && l.q <= kPrefetchUnits && lane < 4)
+            for (int i = 0; i < pc.len; ++i)
+              if (pos + i - k.t * l.q >= p.stages) tma_prefetch_3d(m, c, (pc.k0 + i) * kKB, e);
           for (int i = 0; i < pc.len; ++i) {
             if (lane == 0) {
               ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
@@ -544,13 +562,21 @@ decode_umma_kernel(const __grid_constant__ Params p) {
             finish = sm.last != 0;
             if (finish) {
               __threadfence();
+              // its pieces, four in flight: gate at q, up N * 128 floats on
+              const float* first = p.part_up + entry * entry_of(l, t0, a0) + et;
+              const float* rest = p.part_up + et;
               for (int c = 0; c < cnt; ++c) {
                 float g = 0.f, w = 0.f;
-#pragma unroll 4
-                for (int t = t0; t <= t1; ++t) {
-                  const float* q = p.part_up + entry * entry_of(l, t, a0) + et;
-                  g += __ldcg(q + (size_t)c * 128);
-                  w += __ldcg(q + ((size_t)a.N + c) * 128);
+                for (int t = t0; t <= t1; t += 4) {
+                  float gq[4], wq[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float* q = (t + i == t0 ? first : rest + entry * (2 * (t + i))) + (size_t)c * 128;
+                    gq[i] = t + i <= t1 ? __ldcg(q) : 0.f;
+                    wq[i] = t + i <= t1 ? __ldcg(q + (size_t)a.N * 128) : 0.f;
+                  }
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) { g += gq[i]; w += wq[i]; }
                 }
                 act[(size_t)(r0 + c) * a.F + j * 128 + et] = __float2bfloat16_rn(silu_f(g) * w);
               }
