@@ -146,6 +146,8 @@ decode_route_kernel(const Args a, int S, int wide, int pick) {
   }
   if (s == 0 && g == 0)
     for (int i = tid; i < a.zero_ints; i += kRouteThreads) ((int*)a.cnt)[i] = 0;
+  for (int64_t i = ((int64_t)g * S + s) * kRouteThreads + tid; i < a.fill_vecs; i += (int64_t)gridDim.y * S * kRouteThreads)
+    a.fill[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
   if (!pick) return;                  // the expert kernel goes on from here
   __threadfence();
   __syncthreads();
@@ -408,16 +410,24 @@ size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, 
   const size_t zero = sizeof(Counters) + tiles * sizeof(int);
   void* cnt = take(zero);
   void* part = take(part_bytes(N, H, E));
-  void* act = take((size_t)N * K * F * elem(dt));
+  // the direct variant's activations are fp32
+  const size_t act_row = (size_t)K * F * elem(dt);
+  const size_t direct_rows = (size_t)(N < kDirectTokens ? N : kDirectTokens) * K * F * sizeof(float);
+  const size_t fill0 = off;
+  void* act = take(dt == MOE_BF16 && direct_rows > N * act_row ? direct_rows : N * act_row);
   void* out = take((size_t)N * K * H * sizeof(float));
-  void* pu = dt == MOE_BF16 ? take(umma_part_bytes(N)) : nullptr;
-  void* pd = dt == MOE_BF16 ? take(umma_part_bytes(N)) : nullptr;
+  void* pu = dt == MOE_BF16 ? take(umma_up_bytes(N, H, E, K, F)) : nullptr;
+  void* pd = dt == MOE_BF16 ? take(umma_down_bytes(N, H, E, K, F)) : nullptr;
   if (a) {
     a->status = (int*)base;
     a->arrive = (int*)(base + 64);
     a->queue = (int*)(base + 192);
     a->cnt = (Counters*)cnt;
     a->zero_ints = (int)(zero / sizeof(int));
+    if (dt == MOE_BF16 && N <= kDirectTokens) {
+      a->fill = (uint4*)act;
+      a->fill_vecs = (int64_t)((off - fill0) / sizeof(uint4));
+    }
     w->tile_cnt = (int*)((char*)cnt + sizeof(Counters));
     w->part_up = (float*)pu;
     w->part_down = (float*)pd;

@@ -42,6 +42,8 @@ struct Args {
   int* arrive;                 // [kMaxGroups], inside the status region: zero between calls
   int* queue;                  // bf16: next ticket and blocks that have left, zero between calls too
   Counters* cnt;
+  uint4* fill;                 // words that the router kernel sets to all ones
+  int64_t fill_vecs;
   int zero_ints;               // the router kernel zeroes this many from cnt on
   float* logit_part;           // [groups][S][TG][E]
   void* act;                   // [N*K][F]
@@ -147,7 +149,11 @@ __device__ __forceinline__ void pick_experts(const float* all, int rows, size_t 
 }
 
 // decode_umma.cu: the expert kernel for bf16
-size_t umma_part_bytes(int N);   // partial sums of one phase
+// Up to this many tokens its blocks hand partial sums over without flags, in words
+// that the router kernel has filled with ones (and its activations are fp32).
+constexpr int kDirectTokens = 4;
+size_t umma_up_bytes(int N, int H, int E, int K, int F);     // partial sums of gate and up
+size_t umma_down_bytes(int N, int H, int E, int K, int F);   // of the down product
 moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s);
 
 // ---- plan: which experts are used, by which tokens ---------------------------

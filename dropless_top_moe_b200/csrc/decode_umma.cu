@@ -19,6 +19,15 @@
 // the experts adds them in order while it reads them.  No sum depends on the
 // order in which blocks run.
 //
+// With a few tokens the time is a chain of latencies, and the hand-over between the
+// phases the longest of them: written, fenced, counted, added up, written, fenced,
+// flagged, fetched - 8 us of a 1-token call's 36 (2048/64/6/1408).  Up to kDirectTokens
+// tokens the partial sums carry their own flag instead: the router kernel
+// fills their buffers with a NaN that no sum has (kEmpty), readers poll the very words that they
+// need, and warps 1 and 3 build the down product's token tiles from them.  With more
+// tokens those tiles would be rebuilt from partial sums more often than they
+// are worth.
+//
 // One block an SM, tickets taken in order (decode.cuh says why that cannot
 // deadlock).  Warp 0 takes tickets and streams weights, running up to the whole
 // ring (about 200 KB) ahead: it asks for the down tiles while the activations they
@@ -42,7 +51,8 @@ constexpr int kKB = 64;                     // rows of a unit
 constexpr int kABytes = 4 * 8192;           // four 64 x 64 weight boxes
 constexpr int kMaxStages = 6;
 constexpr int kRing = 8;                    // tickets in flight in a block
-constexpr int kPrefetchUnits = 32;          // longest down ticket whose rest is prefetched
+constexpr int kLongUnits = 16;
+constexpr int kUpTickets = 2, kDownTickets = 4;    // a block, on long lines
 constexpr int kSmemData = 210 * 1024;
 constexpr int kPartFloats = 2 * 128;        // a token's sums of one piece
 
@@ -51,7 +61,7 @@ struct Params {
   CUtensorMap tx;              // [N][H]: one-row boxes, gathered
   CUtensorMap tact;            // [N*K][F]: 16-row boxes
   Args a;
-  float* part_up;              // [2 * tickets][2][N][128]
+  float* part_up;              // [2 * tickets][2][N][128]: a ticket's first piece, its last
   float* part_down;
   int* tile_cnt;               // [slots][F / 128] pieces that have arrived, zeroed by the router
   RouteCut cut;
@@ -63,14 +73,25 @@ struct Params {
 struct Line {
   int nj, kc;      // tiles of a slot, units of a tile
   int units, q, tickets;
+  __device__ __forceinline__ int start(int t) const { return t * q < units ? t * q : units; }
+  __device__ __forceinline__ int ticket_of(int u) const { return u / q; }
+  // Partial-sum entry of ticket t's piece of the tile that starts at unit a.
+  __device__ __forceinline__ int entry(int t, int a) const { return 2 * t + (t * q >= a ? 0 : 1); }
 };
-// Two tickets a block once each is long; one while a second would only add pieces.
-__device__ __forceinline__ Line make_line(int slots, int nj, int kc) {
+// One ticket a block, or `per_block` of them where that leaves two a block at least
+// kLongUnits units each.  More tickets even out the blocks' ends, and cut tiles
+// into more pieces: 2 a block for gate/up and 4 for down measured best (2 and 2: 208 us
+// for 8 tokens 4096/64/4/2048, 200 with 2 and 4, 202 with 4 and 4; a line
+// ending in shorter tickets gained nothing over that).
+__host__ __device__ __forceinline__ int ticket_count(int64_t units, int per_block) {
+  return units >= (int64_t)kBlocks * 2 * kLongUnits ? per_block * kBlocks : kBlocks;
+}
+__device__ __forceinline__ Line make_line(int slots, int nj, int kc, int per_block) {
   Line l;
   l.nj = nj;
   l.kc = kc;
   l.units = slots * nj * kc;
-  const int most = l.units >= kBlocks * 64 ? 2 * kBlocks : kBlocks;
+  const int most = ticket_count(l.units, per_block);
   l.q = (l.units + most - 1) / most;
   l.tickets = (l.units + l.q - 1) / l.q;
   return l;
@@ -86,8 +107,48 @@ __device__ __forceinline__ Piece piece_at(const Line& l, int pos, int end) {
   p.len = l.kc - p.k0 < end - pos ? l.kc - p.k0 : end - pos;
   return p;
 }
-// Partial-sum entry of ticket t's piece of the tile that starts at unit a.
-__device__ __forceinline__ int entry_of(const Line& l, int t, int a) { return 2 * t + (t * l.q >= a ? 0 : 1); }
+// A word that nothing has written yet (direct variant).
+constexpr uint32_t kEmpty = 0xffffffffu;
+__device__ __forceinline__ float not_empty(float v) {
+  return __float_as_uint(v) == kEmpty ? __uint_as_float(0x7fffffffu) : v;
+}
+__device__ __forceinline__ void st_word(float* p, float v) {
+  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(not_empty(v)) : "memory");
+}
+__device__ __forceinline__ float2 ld_words2(const float* p) {
+  float2 v;
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_words4(const float* p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool empty(float2 v) {
+  return __float_as_uint(v.x) == kEmpty || __float_as_uint(v.y) == kEmpty;
+}
+__device__ __forceinline__ bool empty(float4 v) {
+  return __float_as_uint(v.x) == kEmpty || __float_as_uint(v.y) == kEmpty || __float_as_uint(v.z) == kEmpty ||
+         __float_as_uint(v.w) == kEmpty;
+}
+// The limit of a thread that polls words.
+struct Patience {
+  uint64_t t0 = 0;
+  uint32_t it = 0;
+  // another look: false when this thread, or another, gave up
+  __device__ __forceinline__ bool again(Counters* cnt, int* status) {
+    if ((++it & 63) != 0) return true;
+    if (*(volatile int*)&cnt->abort) return false;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 <= kTimeoutNs) return true;
+    *(volatile int*)&cnt->abort = 1;
+    raise_status(status, MOE_DEVERR_TIMEOUT);
+    return false;
+  }
+};
 
 struct Ticket {
   bool up, stop;
@@ -148,6 +209,7 @@ static_assert(kThreads == kRouteThreads, "pick_experts");
 // experts of four columns (thread kl those with k % KL = kl) and are added in
 // order, KL as large as the share leaves threads for: with few columns a block the
 // time is one chain of loads.
+template <bool DIRECT>
 __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const Line& down) {
   const Args& a = p.a;
   const int tid = threadIdx.x;
@@ -171,9 +233,10 @@ __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const
       sm.tile[i][k] = u * down.nj;
     }
   }
-  if (tid == 0) sm.ok = wait_count(&a.cnt->done_down, down.tickets, a.cnt, a.status);
+  if (tid == 0) sm.ok = DIRECT || wait_count(&a.cnt->done_down, down.tickets, a.cnt, a.status);
   __syncthreads();
   if (!sm.ok) return;
+  Patience patience;
   const size_t entry = (size_t)a.N * kPartFloats;
   for (int vb = v0; vb < v1; vb += VL) {
     const int at = vb + vl;
@@ -187,18 +250,25 @@ __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const
         const float w = sm.w[ti][k];
         const int row = sm.row[ti][k];
         const int a0 = (sm.tile[ti][k] + j) * down.kc;
-        const int t0 = a0 / down.q, t1 = (a0 + down.kc - 1) / down.q;
+        const int t0 = down.ticket_of(a0), t1 = down.ticket_of(a0 + down.kc - 1);
         const float* q0 = p.part_down + (size_t)((h >> 7) & 1) * a.N * 128 +
                           (size_t)(row - sm.row0[ti][k]) * 128 + (h & 127);
-        const float* at0 = t0 == t1 ? a.out + (size_t)row * a.H + h : q0 + entry * entry_of(down, t0, a0);
-        float4 o = __ldcg((const float4*)at0);
-        for (int t = t0 + 1; t <= t1; t += 3) {      // three pieces in flight
-          float4 q[3];
+        const float* at0 = t0 == t1 ? a.out + (size_t)row * a.H + h : q0 + entry * down.entry(t0, a0);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int t = t0; t <= t1; t += 4) {          // four pieces in flight
+          float4 q[4];
+          auto piece = [&](int i) { return t + i == t0 ? at0 : q0 + entry * (2 * (t + i)); };
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
-            q[i] = t + i <= t1 ? __ldcg((const float4*)(q0 + entry * (2 * (t + i)))) : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < 4; ++i) {
+            q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t + i <= t1) q[i] = DIRECT ? ld_words4(piece(i)) : __ldcg((const float4*)piece(i));
+          }
 #pragma unroll
-          for (int i = 0; i < 3; ++i) { o.x += q[i].x; o.y += q[i].y; o.z += q[i].z; o.w += q[i].w; }
+          for (int i = 0; i < 4; ++i) {
+            if (DIRECT)
+              while (empty(q[i]) && patience.again(a.cnt, a.status)) q[i] = ld_words4(piece(i));
+            o.x += q[i].x; o.y += q[i].y; o.z += q[i].z; o.w += q[i].w;
+          }
         }
         s.x = fmaf(w, o.x, s.x); s.y = fmaf(w, o.y, s.y); s.z = fmaf(w, o.z, s.z); s.w = fmaf(w, o.w, s.w);
       }
@@ -236,6 +306,7 @@ __device__ __forceinline__ void pick_here(const Params& p, Shared& sm, float* re
   });
 }
 
+template <bool DIRECT>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_umma_kernel(const __grid_constant__ Params p) {
   extern __shared__ unsigned char smem_raw[];
@@ -259,7 +330,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(sm.ring_full[i]), 1);
-      mbar_init(bar(sm.ring_empty[i]), 6);
+      mbar_init(bar(sm.ring_empty[i]), DIRECT ? 7 : 6);
     }
     mbar_init(bar(sm.drain), 1);
     sm.abort = 0;
@@ -295,8 +366,8 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const Line up = make_line(sm.plan.slots, a.F / 128, a.H / kKB);
-  const Line down = make_line(sm.plan.slots, (a.H + 255) / 256, a.F / kKB);
+  const Line up = make_line(sm.plan.slots, a.F / 128, a.H / kKB, kUpTickets);
+  const Line down = make_line(sm.plan.slots, (a.H + 255) / 256, a.F / kKB, kDownTickets);
 
   // the roles' view of the ticket ring
   int slot = 0;
@@ -326,19 +397,14 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       next_slot();
       {
         const Line& l = k.up ? up : down;
-        const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
-        for (int pos = k.t * l.q; pos < end && ok;) {
+        const int begin = l.start(k.t), end = l.start(k.t + 1);
+        for (int pos = begin; pos < end && ok;) {
           const Piece pc = piece_at(l, pos, end);
           const int u = pc.tile / l.nj, j = pc.tile - u * l.nj;
           const int e = sm.plan.expert[u];
           // lane 0-3: one 64-column box each
           const CUtensorMap* m = !k.up ? &p.tw2 : (lane < 2 ? &p.tw1 : &p.tw3);
           const int c = k.up ? j * 128 + (lane & 1) * 64 : j * 256 + lane * 64;
-          // the activations these meet may be some time yet: what the ring cannot
-          // hold of a short ticket waits in L2
-          if (!k.up && l.q <= kPrefetchUnits && lane < 4)
-            for (int i = 0; i < pc.len; ++i)
-              if (pos + i - k.t * l.q >= p.stages) tma_prefetch_3d(m, c, (pc.k0 + i) * kKB, e);
           for (int i = 0; i < pc.len; ++i) {
             if (lane == 0) {
               ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
@@ -367,8 +433,12 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         while (!mbar_try_wait(bar(sm.full_a[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || (DIRECT && warp == 3)) {
     // --------------------------------------------------------- the tokens' rows
+    // (direct variant: of a down ticket's units warp 1 builds the even ones, warp 3 the odd ones)
+    const float* act32 = (const float*)a.act;
+    const size_t entry = (size_t)a.N * kPartFloats;
+    Patience patience;
     int stage = 0;
     uint32_t phase = 0;
     int64_t issued = 0;
@@ -384,12 +454,18 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       next_slot();
       if (k.stop) break;
       const Line& l = k.up ? up : down;
-      const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
-      for (int pos = k.t * l.q; pos < end && ok;) {
+      const int begin = l.start(k.t), end = l.start(k.t + 1);
+      for (int pos = begin; pos < end && ok;) {
         const Piece pc = piece_at(l, pos, end);
         const int u = pc.tile / l.nj;
         const int e = sm.plan.expert[u], r0 = sm.plan.off[u], cnt = sm.plan.off[u + 1] - r0, n16 = round16(cnt);
         int g0 = a.N, g1 = a.N, g2 = a.N, g3 = a.N;        // rows past the last token read as zeros
+        if (k.up && warp == 3) {
+          for (int i = 0; i < pc.len; ++i)
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+          pos += pc.len;
+          continue;
+        }
         if (k.up) {
           for (int n = lane; n < a.N; n += 32)
             if ((sm.plan.mask[e][n >> 5] >> (n & 31)) & 1u) sm.tokens[plan_row(sm.plan, n, e) - r0] = n;
@@ -399,7 +475,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           if (4 * lane + 2 < cnt) g2 = sm.tokens[4 * lane + 2];
           if (4 * lane + 3 < cnt) g3 = sm.tokens[4 * lane + 3];
           __syncwarp();
-        } else if (have != u) {
+        } else if (!DIRECT && have != u) {
           if (lane == 0) {
             ok = wait_count(a.cnt->done_act + u, up.nj, a.cnt, a.status);
             if (!ok) *abort_flag = 1;
@@ -410,6 +486,71 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           have = u;
         }
         for (int i = 0; i < pc.len; ++i) {
+          if (DIRECT && !k.up) {
+            if (((pos + i) & 1) == (warp >> 1)) {
+              // act[r][f] = silu(sum of gate pieces) * (sum of up pieces), lane: f = 2 lane, 2 lane + 1
+              const int f = (pc.k0 + i) * kKB + 2 * lane;
+              const int tile = u * up.nj + (f >> 7), a0 = tile * up.kc;
+              const int t0 = up.ticket_of(a0), t1 = up.ticket_of(a0 + up.kc - 1);
+              const float* first = p.part_up + entry * up.entry(t0, a0) + (f & 127);
+              const float* rest = p.part_up + (f & 127);
+              uint32_t v[kDirectTokens];
+#pragma unroll
+              for (int r = 0; r < kDirectTokens; ++r) v[r] = 0u;
+              auto poll = [&](const float* q) {
+                float2 w = ld_words2(q);
+                while (empty(w) && patience.again(a.cnt, a.status)) w = ld_words2(q);
+                return w;
+              };
+              if (t0 == t1) {
+#pragma unroll
+                for (int r = 0; r < kDirectTokens; ++r)
+                  if (r < cnt) {
+                    const float2 w = poll(act32 + (size_t)(r0 + r) * a.F + f);
+                    v[r] = pack_bf16x2(w.x, w.y);
+                  }
+              } else {
+#pragma unroll
+                for (int r = 0; r < kDirectTokens; ++r)
+                  if (r < cnt) {
+                    float2 g = make_float2(0.f, 0.f), w = g;
+                    for (int t = t0; t <= t1; t += 3) {       // three pieces asked for at once
+                      float2 gq[3], wq[3];
+#pragma unroll
+                      for (int m = 0; m < 3; ++m) {
+                        const float* q = (t + m == t0 ? first : rest + entry * (2 * (t + m))) + r * 128;
+                        gq[m] = t + m <= t1 ? ld_words2(q) : make_float2(0.f, 0.f);
+                        wq[m] = t + m <= t1 ? ld_words2(q + a.N * 128) : make_float2(0.f, 0.f);
+                      }
+#pragma unroll
+                      for (int m = 0; m < 3; ++m) {
+                        const float* q = (t + m == t0 ? first : rest + entry * (2 * (t + m))) + r * 128;
+                        if (empty(gq[m])) gq[m] = poll(q);
+                        if (empty(wq[m])) wq[m] = poll(q + a.N * 128);
+                        g.x += gq[m].x; g.y += gq[m].y;
+                        w.x += wq[m].x; w.y += wq[m].y;
+                      }
+                    }
+                    v[r] = pack_bf16x2(silu_f(g.x) * w.x, silu_f(g.y) * w.y);
+                  }
+              }
+              if (lane == 0) ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
+              ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+              if (!ok) break;
+              const uint32_t dst = base + stage * stage_bytes + kABytes;
+#pragma unroll
+              for (int r = 0; r < kDirectTokens; ++r)      // 128-byte swizzle: 16-byte chunk ^ row
+                if (r < cnt)
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + r * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4),
+                               "r"(v[r])
+                               : "memory");
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(sm.full_b[stage]));
+            }
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            continue;
+          }
           if (lane == 0) {
             ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
             if (ok) mbar_expect_tx(bar(sm.full_b[stage]), n16 * 128);
@@ -450,8 +591,8 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         next_slot();
         if (k.stop) break;
           const Line& l = k.up ? up : down;
-        const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
-        for (int pos = k.t * l.q; pos < end && ok;) {
+        const int begin = l.start(k.t), end = l.start(k.t + 1);
+        for (int pos = begin; pos < end && ok;) {
           const Piece pc = piece_at(l, pos, end);
           const int u = pc.tile / l.nj;
           const int n16 = round16(sm.plan.off[u + 1] - sm.plan.off[u]);
@@ -511,8 +652,8 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       next_slot();
       if (k.stop) break;
       const Line& l = k.up ? up : down;
-      const int end = (k.t + 1) * l.q < l.units ? (k.t + 1) * l.q : l.units;
-      for (int pos = k.t * l.q; pos < end;) {
+      const int begin = l.start(k.t), end = l.start(k.t + 1);
+      for (int pos = begin; pos < end;) {
         const Piece pc = piece_at(l, pos, end);
         const int u = pc.tile / l.nj, j = pc.tile - u * l.nj;
         const int r0 = sm.plan.off[u], cnt = sm.plan.off[u + 1] - r0;
@@ -523,7 +664,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         tc_fence_after();
         const uint32_t d = tmem + acc * 256 + lanes;
         const int a0 = pc.tile * l.kc;
-        float* part = (k.up ? p.part_up : p.part_down) + entry * entry_of(l, k.t, a0) + et;
+        float* part = (k.up ? p.part_up : p.part_down) + entry * l.entry(k.t, a0) + et;
         for (int c = 0; c < cnt; c += 16) {
           uint32_t v0[16], v1[16];
           tmem_ld_16(d + c, v0);
@@ -533,7 +674,19 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           for (int i = 0; i < 16; ++i) {
             if (c + i >= cnt) break;
             const float f0 = __uint_as_float(v0[i]), f1 = __uint_as_float(v1[i]);
-            if (!whole) {
+            if (DIRECT) {
+              const size_t row = r0 + c + i;
+              if (!whole) {
+                st_word(part + (c + i) * 128, f0);
+                st_word(part + (a.N + c + i) * 128, f1);
+              } else if (k.up) {
+                st_word((float*)a.act + row * a.F + j * 128 + et, silu_f(f0) * f1);
+              } else {
+                float* o = a.out + row * a.H + j * 256 + et;
+                st_word(o, f0);
+                if (j * 256 + 128 < a.H) st_word(o + 128, f1);
+              }
+            } else if (!whole) {
               part[(c + i) * 128] = f0;
               part[((size_t)a.N + c + i) * 128] = f1;
             } else if (k.up) {
@@ -550,11 +703,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         if (lane == 0) mbar_arrive(bar(sm.tempty[acc]));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
-        if (k.up) {
+        if (!DIRECT && k.up) {
           bool finish = whole;
           if (!whole) {
             // the last piece of the tile to arrive adds them all
-            const int t0 = a0 / l.q, t1 = (a0 + l.kc - 1) / l.q;
+            const int t0 = l.ticket_of(a0), t1 = l.ticket_of(a0 + l.kc - 1);
             __threadfence();
             epi_barrier();
             if (et == 0) sm.last = atomicAdd(p.tile_cnt + pc.tile, 1) == t1 - t0;
@@ -563,7 +716,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
             if (finish) {
               __threadfence();
               // its pieces, four in flight: gate at q, up N * 128 floats on
-              const float* first = p.part_up + entry * entry_of(l, t0, a0) + et;
+              const float* first = p.part_up + entry * l.entry(t0, a0) + et;
               const float* rest = p.part_up + et;
               for (int c = 0; c < cnt; ++c) {
                 float g = 0.f, w = 0.f;
@@ -592,7 +745,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         pos += pc.len;
       }
       if (!ok) break;
-      if (!k.up) {
+      if (!DIRECT && !k.up) {
         __threadfence();
         epi_barrier();
         if (et == 0) add_release(&a.cnt->done_down, 1);
@@ -602,7 +755,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   tc_fence_before();
   __syncthreads();
   if (warp == 2) tmem_dealloc(tmem, 512);
-  if (!sm.abort) weighted_sums(p, sm, down);
+  if (!sm.abort) weighted_sums<DIRECT>(p, sm, down);
   __syncthreads();
   if (tid == 0) {
     if (sm.abort) *(volatile int*)&a.cnt->abort = 1;
@@ -645,7 +798,17 @@ bool map3(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2
 
 }  // namespace
 
-size_t umma_part_bytes(int N) { return (size_t)(2 * 2 * kBlocks) * N * kPartFloats * sizeof(float); }
+// Buffers of partial sums: no more tickets than the line of every expert that can be used has.
+static int64_t line_units(int N, int K, int E, int nj, int kc) {
+  return (N * (int64_t)K < E ? N * (int64_t)K : E) * nj * kc;
+}
+size_t umma_up_bytes(int N, int H, int E, int K, int F) {
+  return (size_t)2 * ticket_count(line_units(N, K, E, F / 128, H / kKB), kUpTickets) * N * kPartFloats * sizeof(float);
+}
+size_t umma_down_bytes(int N, int H, int E, int K, int F) {
+  return (size_t)2 * ticket_count(line_units(N, K, E, (H + 255) / 256, F / kKB), kDownTickets) * N * kPartFloats *
+         sizeof(float);
+}
 
 moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s) {
   Params p;
@@ -667,8 +830,10 @@ moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, floa
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (cudaFuncSetAttribute(decode_umma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemData + 1024) !=
-        cudaSuccess) {
+    if (cudaFuncSetAttribute(decode_umma_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemData + 1024) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(decode_umma_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemData + 1024) !=
+            cudaSuccess) {
       (void)cudaGetLastError();
       return MOE_ERR_CUDA;
     }
@@ -686,7 +851,10 @@ moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, floa
   cfg.attrs = at;
   cfg.numAttrs = 1;
   cudaError_t err = cudaSuccess;
-  MOE_TRACED("decode_experts_umma", s, (err = cudaLaunchKernelEx(&cfg, decode_umma_kernel, p)));
+  if (a.N <= kDirectTokens)
+    MOE_TRACED("decode_experts_direct", s, (err = cudaLaunchKernelEx(&cfg, decode_umma_kernel<true>, p)));
+  else
+    MOE_TRACED("decode_experts_umma", s, (err = cudaLaunchKernelEx(&cfg, decode_umma_kernel<false>, p)));
   if (err != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;

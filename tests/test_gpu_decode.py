@@ -72,7 +72,7 @@ def run(shape, seed=0, N_max=None):
     return layer, c
 
 
-@pytest.mark.parametrize("N", [1, 2, 7, 8, 9, 16, 17, 33, 64, 100, 128])
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5, 7, 8, 9, 16, 17, 33, 64, 100, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_token_counts(N, dtype):
     run(small_shape("n", N=N, H=256, E=16, K=4, F=384, dtype=dtype), seed=N)
@@ -80,7 +80,8 @@ def test_token_counts(N, dtype):
 
 BF16 = [(5, 128, 1, 1, 128), (9, 128, 2, 1, 256), (3, 256, 5, 5, 128), (40, 384, 7, 3, 640), (20, 512, 256, 8, 128),
         (2, 640, 40, 32, 256), (11, 2048, 64, 6, 1408), (1, 1152, 64, 6, 2944), (128, 128, 3, 2, 1280),
-        (64, 1024, 8, 2, 2048)]
+        (64, 1024, 8, 2, 2048), (1, 1024, 16, 16, 2944), (1, 1024, 32, 32, 2944), (2, 1152, 30, 15, 2816),
+        (3, 2048, 64, 8, 1408), (4, 1024, 40, 10, 2944), (4, 256, 4, 4, 4096), (3, 4096, 1, 1, 256)]
 F32 = [(5, 128, 4, 2, 256), (1, 4, 1, 1, 1), (3, 8, 2, 2, 3), (9, 100, 5, 2, 33), (31, 132, 7, 7, 61), (64, 516, 130, 8, 100),
        (2, 1028, 40, 32, 257), (128, 64, 3, 1, 500), (17, 1000, 12, 3, 1500)]
 
@@ -143,23 +144,30 @@ def test_fewer_tokens_than_the_layer_holds(dtype):
     assert full.shape == (128, 256)
 
 
-def test_values_that_are_not_finite_stay_in_their_rows():
-    shape = small_shape("nan", N=12, H=256, E=16, K=2, F=256)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,bad1,bad2", [(12, 2, 7), (4, 1, 2), (2, 0, 1), (1, 0, 0)])
+def test_values_that_are_not_finite_stay_in_their_rows(N, bad1, bad2, dtype):
+    shape = small_shape("nan", N=N, H=256, E=16, K=2, F=256, dtype=dtype)
     layer, c = run(shape, seed=9)
     clean = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"]).clone()
     top = layer.top_experts.clone()
     bad = c["x"].clone()
-    bad[2] = float("nan")
-    bad[7, 5] = float("inf")
+    bad[bad2, 5] = float("inf")
+    bad[bad1] = float("nan")
     y = layer.forward(bad, c["W_r"], c["W1"], c["W3"], c["W2"])
     torch.cuda.synchronize()
     assert layer.status() == 0
-    keep = [i for i in range(12) if i not in (2, 7)]
+    keep = [i for i in range(N) if i not in (bad1, bad2)]
     assert torch.equal(layer.top_experts[keep], top[keep])
-    assert bool(y[2].isnan().all()) and not bool(torch.isfinite(y[7]).all())
+    assert bool(y[bad1].isnan().all()) and not bool(torch.isfinite(y[bad2]).all())
     assert bool((layer.top_experts >= 0).all()) and bool((layer.top_experts < 16).all())
-    err = (y[keep].double() - clean[keep].double()).abs()
-    assert bool((err <= 2.0 ** -7 * clean[keep].double().abs().amax()).all())
+    for row in layer.top_experts.tolist():
+        assert len(set(row)) == 2
+    if keep:
+        err = (y[keep].double() - clean[keep].double()).abs()
+        assert bool((err <= 2.0 ** -7 * clean[keep].double().abs().amax()).all())
+    y = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"])      # nothing of it is left behind
+    assert torch.equal(y, clean) and layer.status() == 0
 
 
 def test_output_over_the_input_and_into_a_given_buffer():
