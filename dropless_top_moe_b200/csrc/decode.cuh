@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// kRouteThreads threads: the experts and weights of `rows` tokens, at most 8 and
+// A block of kRouteThreads threads or more: the experts and weights of `rows` tokens, at most 8 and
 // at most kRouteCols / EP, EP = 32 V.  Slice q's partial logits of row r start at
 // all + r * row_stride + q * slice_stride; they are added in order.
 // put(row, k, id, weight).  red: 2 * kRouteCols floats.
@@ -86,7 +86,7 @@ __device__ __forceinline__ void pick_experts(const float* all, int rows, size_t 
     const int cv = tid & (CV - 1), sl = tid >> lc, r = cv / QV;
     const float* at = all + r * row_stride + (cv % QV) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows) {
+    if (r < rows && tid < kRouteThreads) {
       for (int q = sl; q < S; q += 8 * SL) {        // eight slices in flight
         float4 o[8];
 #pragma unroll
@@ -103,7 +103,7 @@ __device__ __forceinline__ void pick_experts(const float* all, int rows, size_t 
       v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
     }
     const int lines = CV < 32 ? kRouteThreads / 32 : SL;
-    if (CV >= 32 || lane < CV) ((float4*)red)[(CV < 32 ? warp : sl) * CV + cv] = v;
+    if (tid < kRouteThreads && (CV >= 32 || lane < CV)) ((float4*)red)[(CV < 32 ? warp : sl) * CV + cv] = v;
     __syncthreads();
     for (int i = tid; i < cols; i += kRouteThreads) {
       float t = 0.f;

@@ -47,6 +47,8 @@ using namespace umma;
 
 constexpr int kBlocks = 148;
 constexpr int kThreads = 256;
+constexpr int kBuilders = 6;                // direct variant: warps 1, 3 and four more build token tiles
+constexpr int kDirectThreads = 384;
 constexpr int kKB = 64;                     // rows of a unit
 constexpr int kABytes = 4 * 8192;           // four 64 x 64 weight boxes
 constexpr int kMaxStages = 6;
@@ -203,6 +205,34 @@ struct Shared {
 static_assert(kMaxTokens <= kBlocks, "a block's share of y is at most a row, so it lies in two");
 static_assert(kThreads == kRouteThreads, "pick_experts");
 
+// A block's share of y: vectors [v0, v1) of four columns, and the routing of the
+// one or two tokens that they belong to.
+struct Share {
+  int per_row, v0, v1, first;
+};
+__device__ __forceinline__ Share share_of(const Args& a) {
+  Share h;
+  h.per_row = a.H / 4;
+  const int vecs = a.N * h.per_row, share = (vecs + kBlocks - 1) / kBlocks;
+  h.v0 = (int)blockIdx.x * share;
+  h.v1 = h.v0 + share < vecs ? h.v0 + share : vecs;
+  h.first = h.v0 / h.per_row;
+  return h;
+}
+// Thread i of 2 K: expert i % K of the share's token i / K.
+__device__ __forceinline__ void prepare_sum(const Args& a, Shared& sm, const Line& down, int i) {
+  const Share h = share_of(a);
+  const int ti = i / a.K, k = i - ti * a.K, n = h.first + ti;
+  if (h.v0 >= h.v1 || n >= a.N) return;
+  const bool here = a.N <= kPickTokens;
+  const int e = here ? sm.pick_id[n][k] : __ldcg(a.top + n * a.K + k);
+  const int u = sm.plan.slot_of[e];
+  sm.w[ti][k] = here ? sm.pick_w[n][k] : __ldcg(a.weights + n * a.K + k);
+  sm.row[ti][k] = plan_row(sm.plan, n, e);
+  sm.row0[ti][k] = sm.plan.off[u];
+  sm.tile[ti][k] = u * down.nj;
+}
+
 // y[n] = sum_k w[n,k] out[row(n,k)], each out from its pieces in order.  Every
 // block takes its share of the columns; nothing waits for it.  What does not
 // depend on the down product is ready before the wait.  KL threads share the
@@ -213,26 +243,12 @@ template <bool DIRECT>
 __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const Line& down) {
   const Args& a = p.a;
   const int tid = threadIdx.x;
-  const int per_row = a.H / 4, vecs = a.N * per_row;
-  const int share = (vecs + kBlocks - 1) / kBlocks;
-  const int v0 = (int)blockIdx.x * share, v1 = v0 + share < vecs ? v0 + share : vecs;
+  const Share sh = share_of(a);
+  const int per_row = sh.per_row, v0 = sh.v0, v1 = sh.v1, share = v1 - v0, first = sh.first;
   if (v0 >= v1) return;
   int KL = 1;
   while (KL < 8 && KL < a.K && 2 * KL * share <= kThreads) KL *= 2;
   const int VL = kThreads / KL, vl = tid % VL, kl = tid / VL;
-  const int first = v0 / per_row;
-  if (tid < 2 * a.K) {
-    const int i = tid / a.K, k = tid - i * a.K, n = first + i;
-    if (n < a.N) {
-      const bool here = a.N <= kPickTokens;
-      const int e = here ? sm.pick_id[n][k] : __ldcg(a.top + n * a.K + k);
-      const int u = sm.plan.slot_of[e];
-      sm.w[i][k] = here ? sm.pick_w[n][k] : __ldcg(a.weights + n * a.K + k);
-      sm.row[i][k] = plan_row(sm.plan, n, e);
-      sm.row0[i][k] = sm.plan.off[u];
-      sm.tile[i][k] = u * down.nj;
-    }
-  }
   if (tid == 0) sm.ok = DIRECT || wait_count(&a.cnt->done_down, down.tickets, a.cnt, a.status);
   __syncthreads();
   if (!sm.ok) return;
@@ -240,7 +256,7 @@ __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const
   const size_t entry = (size_t)a.N * kPartFloats;
   for (int vb = v0; vb < v1; vb += VL) {
     const int at = vb + vl;
-    const bool in = at < v1;
+    const bool in = at < v1 && tid < kThreads;
     const int n = in ? at / per_row : first, h = in ? (at - n * per_row) * 4 : 0;
     const int ti = n - first, j = h >> 8;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -274,9 +290,9 @@ __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const
       }
     }
     if (KL > 1) {
-      sm.sum[tid] = s;
+      if (tid < kThreads) sm.sum[tid] = s;
       __syncthreads();
-      if (kl == 0) {
+      if (kl == 0 && in) {
         for (int i = 1; i < KL; ++i) {
           const float4 q = sm.sum[i * VL + vl];
           s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
@@ -307,7 +323,7 @@ __device__ __forceinline__ void pick_here(const Params& p, Shared& sm, float* re
 }
 
 template <bool DIRECT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(DIRECT ? kDirectThreads : kThreads, 1)
 decode_umma_kernel(const __grid_constant__ Params p) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ Shared sm;
@@ -330,7 +346,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(sm.ring_full[i]), 1);
-      mbar_init(bar(sm.ring_empty[i]), DIRECT ? 7 : 6);
+      mbar_init(bar(sm.ring_empty[i]), DIRECT ? 5 + kBuilders : 6);
     }
     mbar_init(bar(sm.drain), 1);
     sm.abort = 0;
@@ -347,7 +363,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   // first one can be taken while the router still runs
   int v = 0;
   if (tid == 0) v = atomicAdd(a.queue, 1);
-  clear_plan(sm.plan, kThreads);
+  clear_plan(sm.plan, (int)blockDim.x);
   pdl_wait();
   if (a.N <= kPickTokens) {
     float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));   // the ring is still empty
@@ -357,10 +373,10 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       case 128: pick_here<4>(p, sm, red); break;
       default: pick_here<8>(p, sm, red); break;
     }
-    build_plan(sm.plan, nullptr, a.N, a.K, a.E, kThreads);
+    build_plan(sm.plan, nullptr, a.N, a.K, a.E, (int)blockDim.x);
     fence_proxy_async();       // `red` was written where TMA will write
   } else {
-    build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
+    build_plan(sm.plan, a.top, a.N, a.K, a.E, (int)blockDim.x);
   }
   tc_fence_before();
   __syncthreads();
@@ -368,6 +384,9 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   const uint32_t tmem = sm.tmem;
   const Line up = make_line(sm.plan.slots, a.F / 128, a.H / kKB, kUpTickets);
   const Line down = make_line(sm.plan.slots, (a.H + 255) / 256, a.F / kKB, kDownTickets);
+
+  if (warp == (DIRECT ? kDirectThreads / 32 - 1 : 3))
+    for (int i = lane; i < 2 * a.K; i += 32) prepare_sum(a, sm, down, i);
 
   // the roles' view of the ticket ring
   int slot = 0;
@@ -433,9 +452,10 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         while (!mbar_try_wait(bar(sm.full_a[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
       }
     }
-  } else if (warp == 1 || (DIRECT && warp == 3)) {
+  } else if (warp == 1 || (DIRECT && (warp == 3 || warp >= 8))) {
     // --------------------------------------------------------- the tokens' rows
-    // (direct variant: of a down ticket's units warp 1 builds the even ones, warp 3 the odd ones)
+    // (direct variant: the builders take a down ticket's units in turn)
+    const int builder = warp == 1 ? 0 : (warp == 3 ? 1 : warp - 6);
     const float* act32 = (const float*)a.act;
     const size_t entry = (size_t)a.N * kPartFloats;
     Patience patience;
@@ -460,7 +480,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         const int u = pc.tile / l.nj;
         const int e = sm.plan.expert[u], r0 = sm.plan.off[u], cnt = sm.plan.off[u + 1] - r0, n16 = round16(cnt);
         int g0 = a.N, g1 = a.N, g2 = a.N, g3 = a.N;        // rows past the last token read as zeros
-        if (k.up && warp == 3) {
+        if (DIRECT && k.up && builder != 0) {
           for (int i = 0; i < pc.len; ++i)
             if (++stage == p.stages) { stage = 0; phase ^= 1u; }
           pos += pc.len;
@@ -487,7 +507,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         }
         for (int i = 0; i < pc.len; ++i) {
           if (DIRECT && !k.up) {
-            if (((pos + i) & 1) == (warp >> 1)) {
+            if ((pos + i) % kBuilders == builder) {
               // act[r][f] = silu(sum of gate pieces) * (sum of up pieces), lane: f = 2 lane, 2 lane + 1
               const int f = (pc.k0 + i) * kKB + 2 * lane;
               const int tile = u * up.nj + (f >> 7), a0 = tile * up.kc;
@@ -497,36 +517,42 @@ decode_umma_kernel(const __grid_constant__ Params p) {
               uint32_t v[kDirectTokens];
 #pragma unroll
               for (int r = 0; r < kDirectTokens; ++r) v[r] = 0u;
-              auto poll = [&](const float* q) {
-                float2 w = ld_words2(q);
-                while (empty(w) && patience.again(a.cnt, a.status)) w = ld_words2(q);
-                return w;
-              };
               if (t0 == t1) {
+                float2 w[kDirectTokens];
+                bool miss;
+                do {
+                  miss = false;
+#pragma unroll
+                  for (int r = 0; r < kDirectTokens; ++r)
+                    if (r < cnt) w[r] = ld_words2(act32 + (size_t)(r0 + r) * a.F + f);
+#pragma unroll
+                  for (int r = 0; r < kDirectTokens; ++r)
+                    if (r < cnt) miss |= empty(w[r]);
+                } while (miss && patience.again(a.cnt, a.status));
 #pragma unroll
                 for (int r = 0; r < kDirectTokens; ++r)
-                  if (r < cnt) {
-                    const float2 w = poll(act32 + (size_t)(r0 + r) * a.F + f);
-                    v[r] = pack_bf16x2(w.x, w.y);
-                  }
+                  if (r < cnt) v[r] = pack_bf16x2(w[r].x, w[r].y);
               } else {
 #pragma unroll
                 for (int r = 0; r < kDirectTokens; ++r)
                   if (r < cnt) {
                     float2 g = make_float2(0.f, 0.f), w = g;
-                    for (int t = t0; t <= t1; t += 3) {       // three pieces asked for at once
-                      float2 gq[3], wq[3];
+                    for (int t = t0; t <= t1; t += 4) {       // four pieces asked for at once
+                      float2 gq[4], wq[4];
+                      bool miss;
+                      do {
+                        miss = false;
 #pragma unroll
-                      for (int m = 0; m < 3; ++m) {
-                        const float* q = (t + m == t0 ? first : rest + entry * (2 * (t + m))) + r * 128;
-                        gq[m] = t + m <= t1 ? ld_words2(q) : make_float2(0.f, 0.f);
-                        wq[m] = t + m <= t1 ? ld_words2(q + a.N * 128) : make_float2(0.f, 0.f);
-                      }
+                        for (int m = 0; m < 4; ++m) {
+                          const float* q = (t + m == t0 ? first : rest + entry * (2 * (t + m))) + r * 128;
+                          gq[m] = t + m <= t1 ? ld_words2(q) : make_float2(0.f, 0.f);
+                          wq[m] = t + m <= t1 ? ld_words2(q + a.N * 128) : make_float2(0.f, 0.f);
+                        }
 #pragma unroll
-                      for (int m = 0; m < 3; ++m) {
-                        const float* q = (t + m == t0 ? first : rest + entry * (2 * (t + m))) + r * 128;
-                        if (empty(gq[m])) gq[m] = poll(q);
-                        if (empty(wq[m])) wq[m] = poll(q + a.N * 128);
+                        for (int m = 0; m < 4; ++m) miss |= empty(gq[m]) || empty(wq[m]);
+                      } while (miss && patience.again(a.cnt, a.status));
+#pragma unroll
+                      for (int m = 0; m < 4; ++m) {
                         g.x += gq[m].x; g.y += gq[m].y;
                         w.x += wq[m].x; w.y += wq[m].y;
                       }
@@ -633,7 +659,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     // ---------------------------------------------------------------- epilogue
     const int et = tid - 128, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -842,7 +868,7 @@ moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, floa
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(kBlocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(a.N <= kDirectTokens ? kDirectThreads : kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
