@@ -24,7 +24,7 @@
 // flagged, fetched - 8 us of a 1-token call's 36 (2048/64/6/1408).  Up to kDirectTokens
 // tokens the partial sums carry their own flag instead: the router kernel
 // fills their buffers with a NaN that no sum has (kEmpty), readers poll the very words that they
-// need, and warps 1 and 3 build the down product's token tiles from them.  With more
+// need, and five warps build the down product's token tiles from them.  With more
 // tokens those tiles would be rebuilt from partial sums more often than they
 // are worth.
 //
@@ -32,8 +32,8 @@
 // deadlock).  Warp 0 takes tickets and streams weights, running up to the whole
 // ring (about 200 KB) ahead: it asks for the down tiles while the activations they
 // meet are still being computed.  Warp 1 brings the tokens' rows: TMA row gathers of
-// x, or rows of the activations once their slot is complete.  Warp 2 issues the MMAs, warps
-// 4-7 read TMEM (two accumulator sets) and write.
+// x, or rows of the activations once their slot is complete.  Warps 2 and 3 issue
+// the MMAs of one tile each, warps 4-7 read TMEM (two accumulator sets) and write.
 #include <cuda.h>
 #include <string.h>
 
@@ -47,7 +47,7 @@ using namespace umma;
 
 constexpr int kBlocks = 148;
 constexpr int kThreads = 256;
-constexpr int kBuilders = 6;                // direct variant: warps 1, 3 and four more build token tiles
+constexpr int kBuilders = 5;                // direct variant: warp 1 and four more build token tiles
 constexpr int kDirectThreads = 384;
 constexpr int kKB = 64;                     // rows of a unit
 constexpr int kABytes = 4 * 8192;           // four 64 x 64 weight boxes
@@ -186,10 +186,10 @@ __device__ __forceinline__ bool epi_all(bool yes) {
 struct Shared {
   Plan plan;
   int tokens[kMaxTokens];      // warp 1's current slot
-  uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2];
   uint64_t ring_full[kRing], ring_empty[kRing];
-  uint64_t drain;
+  uint64_t drain[2];
   int ring[kRing];
   uint32_t tmem;
   int abort;
@@ -336,19 +336,19 @@ decode_umma_kernel(const __grid_constant__ Params p) {
 
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(bar(sm.full_a[i]), 1);
-      mbar_init(bar(sm.full_b[i]), 1);
-      mbar_init(bar(sm.empty[i]), 1);
+      mbar_init(bar(sm.full[i]), 2);         // the weights' producer and the tokens'
+      mbar_init(bar(sm.empty[i]), 2);        // both MMA warps
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(sm.tfull[i]), 1);
+      mbar_init(bar(sm.tfull[i]), 2);
       mbar_init(bar(sm.tempty[i]), 4);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(sm.ring_full[i]), 1);
-      mbar_init(bar(sm.ring_empty[i]), DIRECT ? 5 + kBuilders : 6);
+      mbar_init(bar(sm.ring_empty[i]), 2 + 4 + (DIRECT ? kBuilders : 1));   // MMA, epilogue, tokens' rows
     }
-    mbar_init(bar(sm.drain), 1);
+    mbar_init(bar(sm.drain[0]), 1);
+    mbar_init(bar(sm.drain[1]), 1);
     sm.abort = 0;
     fence_barrier_init();
   } else if (warp == 1 && lane < 5) {
@@ -385,7 +385,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   const Line up = make_line(sm.plan.slots, a.F / 128, a.H / kKB, kUpTickets);
   const Line down = make_line(sm.plan.slots, (a.H + 255) / 256, a.F / kKB, kDownTickets);
 
-  if (warp == (DIRECT ? kDirectThreads / 32 - 1 : 3))
+  if (warp == (DIRECT ? kDirectThreads / 32 - 1 : 4))
     for (int i = lane; i < 2 * a.K; i += 32) prepare_sum(a, sm, down, i);
 
   // the roles' view of the ticket ring
@@ -427,12 +427,12 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           for (int i = 0; i < pc.len; ++i) {
             if (lane == 0) {
               ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
-              if (ok) mbar_expect_tx(bar(sm.full_a[stage]), kABytes);
+              if (ok) mbar_expect_tx(bar(sm.full[stage]), kABytes);
             }
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             if (!ok) break;
             if (lane < 4)
-              tma_load_3d(base + stage * stage_bytes + lane * 8192, m, bar(sm.full_a[stage]), c, (pc.k0 + i) * kKB, e);
+              tma_load_3d(base + stage * stage_bytes + lane * 8192, m, bar(sm.full[stage]), c, (pc.k0 + i) * kKB, e);
             ++issued;
             if (++stage == p.stages) { stage = 0; phase ^= 1u; }
           }
@@ -449,13 +449,13 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       for (int i = 0; i < p.stages && i < issued; ++i) {
         if (stage-- == 0) { stage = p.stages - 1; phase ^= 1u; }
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(bar(sm.full_a[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
+        while (!mbar_try_wait(bar(sm.full[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
       }
     }
-  } else if (warp == 1 || (DIRECT && (warp == 3 || warp >= 8))) {
+  } else if (warp == 1 || (DIRECT && warp >= 8)) {
     // --------------------------------------------------------- the tokens' rows
     // (direct variant: the builders take a down ticket's units in turn)
-    const int builder = warp == 1 ? 0 : (warp == 3 ? 1 : warp - 6);
+    const int builder = warp == 1 ? 0 : warp - 7;
     const float* act32 = (const float*)a.act;
     const size_t entry = (size_t)a.N * kPartFloats;
     Patience patience;
@@ -572,23 +572,23 @@ decode_umma_kernel(const __grid_constant__ Params p) {
                                : "memory");
               fence_proxy_async();
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar(sm.full_b[stage]));
+              if (lane == 0) mbar_arrive(bar(sm.full[stage]));
             }
             if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             continue;
           }
           if (lane == 0) {
             ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
-            if (ok) mbar_expect_tx(bar(sm.full_b[stage]), n16 * 128);
+            if (ok) mbar_expect_tx(bar(sm.full[stage]), n16 * 128);
           }
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
           if (!ok) break;
           const uint32_t dst = base + stage * stage_bytes + kABytes;
           const int kcol = (pc.k0 + i) * kKB;
           if (k.up) {
-            if (4 * lane < n16) tma_gather4(dst + lane * 512, &p.tx, bar(sm.full_b[stage]), kcol, g0, g1, g2, g3);
+            if (4 * lane < n16) tma_gather4(dst + lane * 512, &p.tx, bar(sm.full[stage]), kcol, g0, g1, g2, g3);
           } else {
-            if (16 * lane < n16) tma_load_2d(dst + lane * 2048, &p.tact, bar(sm.full_b[stage]), kcol, r0 + 16 * lane);
+            if (16 * lane < n16) tma_load_2d(dst + lane * 2048, &p.tact, bar(sm.full[stage]), kcol, r0 + 16 * lane);
           }
           ++issued;
           if (++stage == p.stages) { stage = 0; phase ^= 1u; }
@@ -600,11 +600,15 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       for (int i = 0; i < p.stages && i < issued; ++i) {
         if (stage-- == 0) { stage = p.stages - 1; phase ^= 1u; }
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(bar(sm.full_b[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
+        while (!mbar_try_wait(bar(sm.full[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
       }
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 || warp == 3) {
     // --------------------------------------------------------------------- MMA
+    // One thread takes some 75 cycles an MMA, about 800 a unit for both of its tiles,
+    // and a ring that fills at once (activations that were waited for) empties no
+    // faster: so a thread a tile.
+    const int half = warp - 2;
     if (lane == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
@@ -626,21 +630,15 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           ok = mbar_wait_bounded(bar(sm.tempty[acc]), acc_phase ^ 1u, abort_flag, a.status, kTimeoutNs);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d = tmem + acc * 256;
+          const uint32_t d = tmem + acc * 256 + half * 128;
           for (int i = 0; i < pc.len; ++i) {
-            ok = mbar_wait_bounded(bar(sm.full_a[stage]), phase, abort_flag, a.status, kTimeoutNs) &&
-                 mbar_wait_bounded(bar(sm.full_b[stage]), phase, abort_flag, a.status, kTimeoutNs);
+            ok = mbar_wait_bounded(bar(sm.full[stage]), phase, abort_flag, a.status, kTimeoutNs);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sa = base + stage * stage_bytes, sb = sa + kABytes;
+            const uint32_t sa = base + stage * stage_bytes + half * 16384, sb = base + stage * stage_bytes + kABytes;
 #pragma unroll
-            for (int kk = 0; kk < kKB / 16; ++kk) {
-              const uint64_t bd = desc_k_sw128(sb + kk * 32);
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                mma_bf16(d + h * 128, desc_mn_sw128(sa + h * 16384 + kk * 2048, 8192), bd, idesc,
-                         (i | kk) != 0 ? 1u : 0u);
-            }
+            for (int kk = 0; kk < kKB / 16; ++kk)
+              mma_bf16(d, desc_mn_sw128(sa + kk * 2048, 8192), desc_k_sw128(sb + kk * 32), idesc, (i | kk) != 0 ? 1u : 0u);
             mma_commit(bar(sm.empty[stage]));
             if (++stage == p.stages) { stage = 0; phase ^= 1u; }
           }
@@ -653,9 +651,9 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       }
       if (*abort_flag) {
         // the MMAs in flight still read shared memory and write TMEM
-        mma_commit(bar(sm.drain));
+        mma_commit(bar(sm.drain[half]));
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(bar(sm.drain), 0) && globaltimer() - t0 < 50000000ull) {}
+        while (!mbar_try_wait(bar(sm.drain[half]), 0) && globaltimer() - t0 < 50000000ull) {}
       }
     }
     __syncwarp();
