@@ -12,11 +12,7 @@
 // slice's partial logits, and the last block of a group to arrive adds the
 // slices in order and picks the experts, a warp a token.
 //
-// Expert kernel (fp32): blocks take tickets in order - gate/up tiles of every
-// used expert, then down tiles, then the weighted sums - and wait only for
-// lower tickets.  A tile is 16 vectors of columns; 16 groups of threads share the
-// rows, 4 tokens at a time, and are added in order, so results have the same
-// bits on every run.
+// Expert kernels: below for fp32, decode_umma.cu for bf16.
 #include <math.h>
 #include <string.h>
 
@@ -166,187 +162,245 @@ decode_route_kernel(const Args a, int S, int wide, int pick) {
                });
 }
 
-// ---- experts, one block of 256 threads a tile --------------------------------
+// ---- fp32 experts ------------------------------------------------------------
+// fp32 layers keep full single precision, so their products are FMAs.  A block
+// takes a tile of 4 CT columns (gate and up of the same ones, or down), its 256 / CT
+// row groups stream the rows, 16-byte loads, up to 16 of them in flight, and TM
+// tokens share each weight; the groups' sums are added in a fixed order.  Activations and
+// expert outputs are handed over as words that are their own flags, tiles as
+// tickets in order, so the phases run into each other.  HBM bounds it up to some
+// eight tokens an expert, FMAs beyond.
 constexpr int kThreads = 256;
-constexpr int kColThreads = 16, kRowGroups = kThreads / kColThreads;
-constexpr int kTM = 4;               // tokens at a time
 constexpr int kXRows = 512;          // rows of the tokens' operand staged at a time
+constexpr int kTokens = 8;           // most tokens at a time
 
-// V columns of a weight row from column c on: one 16-byte load, or (rows that
-// are not a whole number of vectors long) element by element.
-template <typename T, bool WIDE>
-__device__ __forceinline__ void load_w(const T* row, int ct, int c0, int cols, float* f) {
-  constexpr int V = Vec<T>::N;
+// Four columns of a weight row: one 16-byte load, or (rows that are not a whole
+// number of vectors long) element by element.
+template <int CT, bool WIDE>
+__device__ __forceinline__ float4 load_w(const float* row, int ct, int c0, int cols) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (WIDE) {
-    const int c = c0 + ct * V;
-    if (c < cols) {
-      Vec<T>::to_float(ld_nc_v4(row + c), f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) f[j] = 0.f;
-    }
+    if (c0 + ct * 4 < cols) v = __ldg((const float4*)(row + c0 + ct * 4));
   } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = c0 + j * kColThreads + ct;
-      f[j] = c < cols ? to_f<T>(row[c]) : 0.f;
-    }
+    const int c = c0 + ct;
+    if (c < cols) v.x = __ldg(row + c);
+    if (c + CT < cols) v.y = __ldg(row + c + CT);
+    if (c + 2 * CT < cols) v.z = __ldg(row + c + 2 * CT);
+    if (c + 3 * CT < cols) v.w = __ldg(row + c + 3 * CT);
   }
+  return v;
 }
-template <bool WIDE, int V>
+template <int CT, bool WIDE>
 __device__ __forceinline__ int tile_col(int ct, int j) {
-  return WIDE ? ct * V + j : j * kColThreads + ct;
+  return WIDE ? ct * 4 + j : j * CT + ct;
 }
 
 struct Smem {
   Plan plan;
+  Picked pick;
   int tokens[kMaxTokens];
-  float xs[kTM][kXRows];
-  float red[2][kRowGroups][kColThreads * 8];
+  alignas(16) float xs[kTokens][kXRows];
+  alignas(16) float red[8][kTokens * 2 * 64];    // a warp's sums: [token][matrix][column]
   int ticket;
   int ok;
 };
+static_assert(sizeof(((Smem*)0)->red) >= 2 * kRouteCols * sizeof(float), "pick_experts' scratch");
 
-// One tile of NM matrices (gate and up, or down) for all tokens of a slot:
-// C_m[t][c] = sum_r in[t][r] W_m[r][c]; `in` gives the operand's element, `put`
-// takes the NM sums of a (token, column).
-template <typename T, bool WIDE, int NM, class In, class Put>
-__device__ __forceinline__ void tile(Smem& sm, const T* const (&W)[NM], int depth, int cols, int c0, int cnt, In in,
-                                     Put put) {
-  constexpr int V = Vec<T>::N, kCols = kColThreads * V;
-  const int tid = threadIdx.x, ct = tid % kColThreads, rg = tid / kColThreads;
-  for (int t0 = 0; t0 < cnt; t0 += kTM) {
-    float acc[kTM][NM][V];
+// A tile of NM matrices for TM tokens from row t0 of a slot on:
+// C_m[t][c] = sum_r in(t, r) W_m[r][c]; put(t, c, sums) takes them.  POLL: `in` gives
+// words that may still be empty.
+template <int CT, bool WIDE, bool POLL, int NM, int TM, class In, class Put>
+__device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, Smem& sm, const float* const (&W)[NM], int depth, int cols, int c0, int t0,
+                                            int cnt, In in, Put put) {
+  constexpr int RG = kThreads / CT, U = TM > 4 ? 4 : 8;   // rows in flight a thread
+  const int tid = threadIdx.x, ct = tid % CT, rg = tid / CT, warp = tid >> 5, lane = tid & 31;
+  float acc[TM][NM][4];
 #pragma unroll
-    for (int t = 0; t < kTM; ++t)
+  for (int t = 0; t < TM; ++t)
 #pragma unroll
-      for (int m = 0; m < NM; ++m)
+    for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[t][m][j] = 0.f;
-    for (int r0 = 0; r0 < depth; r0 += kXRows) {
-      const int rows = depth - r0 < kXRows ? depth - r0 : kXRows;
-      __syncthreads();
-      for (int i = tid; i < kTM * kXRows; i += kThreads) {
-        const int q = i / kXRows, r = i % kXRows;
-        sm.xs[q][r] = t0 + q < cnt && r < rows ? in(t0 + q, r0 + r) : 0.f;
+      for (int j = 0; j < 4; ++j) acc[t][m][j] = 0.f;
+  for (int r0 = 0; r0 < depth; r0 += kXRows) {
+    const int rows = depth - r0 < kXRows ? depth - r0 : kXRows;
+    __syncthreads();
+    for (int i0 = tid; i0 < TM * rows; i0 += 8 * kThreads) {      // eight values in flight
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * kThreads, t = i / rows;
+        v[j] = i < TM * rows && t0 + t < cnt ? in(t0 + t, r0 + i - t * rows) : 0.f;
       }
-      __syncthreads();
-#pragma unroll 4
-      for (int r = rg; r < rows; r += kRowGroups) {
-        float w[NM][V];
 #pragma unroll
-        for (int m = 0; m < NM; ++m) load_w<T, WIDE>(W[m] + (size_t)(r0 + r) * cols, ct, c0, cols, w[m]);
-#pragma unroll
-        for (int t = 0; t < kTM; ++t) {
-          const float xv = sm.xs[t][r];
-#pragma unroll
-          for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int j = 0; j < V; ++j) acc[t][m][j] = fmaf(xv, w[m][j], acc[t][m][j]);
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * kThreads, t = i / rows;
+        if (i < TM * rows) {
+          if (POLL)
+            while (__float_as_uint(v[j]) == kEmpty && patience.again(a.cnt, a.status)) v[j] = in(t0 + t, r0 + i - t * rows);
+          sm.xs[t][i - t * rows] = v[j];
         }
       }
     }
-    // the row groups' sums, in order
-    for (int t = 0; t < kTM && t0 + t < cnt; ++t) {
-      __syncthreads();
+    __syncthreads();
+    for (int rb = rg; rb < rows; rb += RG * U) {
+      float4 w[U][NM];
 #pragma unroll
-      for (int q = 0; q < kTM; ++q)
-        if (q == t) {
-#pragma unroll
-          for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int j = 0; j < V; ++j) sm.red[m][rg][tile_col<WIDE, V>(ct, j)] = acc[q][m][j];
-        }
-      __syncthreads();
-      if (tid < kCols && c0 + tid < cols) {
-        float v[NM];
+      for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-          v[m] = 0.f;
-#pragma unroll
-          for (int q = 0; q < kRowGroups; ++q) v[m] += sm.red[m][q][tid];
+          w[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (rb + i * RG < rows) w[i][m] = load_w<CT, WIDE>(W[m] + (size_t)(r0 + rb + i * RG) * cols, ct, c0, cols);
         }
-        put(t0 + t, c0 + tid, v);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (rb + i * RG < rows) {
+#pragma unroll
+          for (int t = 0; t < TM; ++t) {
+            const float xv = sm.xs[t][rb + i * RG];
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+              acc[t][m][0] = fmaf(xv, w[i][m].x, acc[t][m][0]);
+              acc[t][m][1] = fmaf(xv, w[i][m].y, acc[t][m][1]);
+              acc[t][m][2] = fmaf(xv, w[i][m].z, acc[t][m][2]);
+              acc[t][m][3] = fmaf(xv, w[i][m].w, acc[t][m][3]);
+            }
+          }
+        }
       }
+    }
+  }
+  // the row groups of a warp, then the warps, each in a fixed order
+  constexpr int C = 4 * CT;
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v = acc[t][m][j];
+#pragma unroll
+        for (int o = CT; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane < CT) sm.red[warp][(t * NM + m) * C + tile_col<CT, WIDE>(ct, j)] = v;
+      }
+  __syncthreads();
+  for (int i = tid; i < TM * C; i += kThreads) {
+    const int t = i / C, c = i - t * C;
+    if (t0 + t < cnt && c0 + c < cols) {
+      float v[NM];
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        v[m] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[m] += sm.red[q][(t * NM + m) * C + c];
+      }
+      put(t0 + t, c0 + c, v);
+    }
+  }
+}
+template <int CT, bool WIDE, bool POLL, int NM, class In, class Put>
+__device__ __forceinline__ void tile(const Args& a, Patience& patience, Smem& sm, const float* const (&W)[NM], int depth, int cols, int c0, int cnt, In in,
+                                     Put put) {
+  for (int t0 = 0; t0 < cnt;) {
+    const int left = cnt - t0;
+    if (left == 1) {
+      tile_tokens<CT, WIDE, POLL, NM, 1>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
+      t0 += 1;
+    } else if (left <= 4) {
+      tile_tokens<CT, WIDE, POLL, NM, 4>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
+      t0 += 4;
+    } else {
+      tile_tokens<CT, WIDE, POLL, NM, 8>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
+      t0 += 8;
     }
   }
 }
 
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads)
-decode_experts_kernel(const Args a) {
-  __shared__ Smem sm;
-  constexpr int V = Vec<T>::N, kCols = kColThreads * V;
+template <int CT, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 2)
+decode_experts_kernel(const Args a, const RouteCut cut) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  constexpr int C = 4 * CT;
   const int tid = threadIdx.x;
-  const T* x = (const T*)a.x;
-  T* act = (T*)a.act;
+  const float* x = (const float*)a.x;
+  float* act = (float*)a.act;
+  // tickets start at zero (the previous call's last block left them so), so the
+  // first one can be taken while the router still runs
+  if (tid == 0) sm.ticket = atomicAdd(a.queue, 1);
   clear_plan(sm.plan, kThreads);
   pdl_wait();
-  build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
+  if (cut.here) {
+    pick_all(a, cut, sm.plan, sm.pick, &sm.red[0][0]);
+    build_plan(sm.plan, nullptr, a.N, a.K, a.E, kThreads);
+  } else {
+    build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
+  }
   const int slots = sm.plan.slots;
-  const int nft = (int)cdiv(a.F, kCols), nht = (int)cdiv(a.H, kCols);
+  const int nft = (int)cdiv(a.F, C), nht = (int)cdiv(a.H, C);
   const int n_up = slots * nft, n_down = slots * nht;
-  const int64_t vecs = (int64_t)a.N * (a.H / V);
-  const int n_sum = (int)cdiv(vecs, kThreads);
+  Patience patience;
   for (;;) {
-    __syncthreads();
-    if (tid == 0) sm.ticket = atomicAdd(&a.cnt->ticket, 1);
-    __syncthreads();
     int t = sm.ticket;
-    if (t >= n_up + n_down + n_sum) return;
-    if (t >= n_up + n_down) {
-      // y[n] = sum_k w[n,k] out[row(n,k)], in increasing k
-      t -= n_up + n_down;
-      if (tid == 0) sm.ok = wait_count(&a.cnt->done_down, n_down, a.cnt, a.status);
-      __syncthreads();
-      if (!sm.ok) return;
-      const int64_t at = (int64_t)t * kThreads + tid;
-      if (at < vecs) {
-        const int n = (int)(at / (a.H / V)), h = (int)(at % (a.H / V)) * V;
-        float s[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[j] = 0.f;
-        for (int k = 0; k < a.K; ++k) {
-          const int e = __ldcg(a.top + (size_t)n * a.K + k);
-          const float w = __ldcg(a.weights + (size_t)n * a.K + k);
-          const float* o = a.out + (size_t)plan_row(sm.plan, n, e) * a.H + h;
-#pragma unroll
-          for (int j = 0; j < V; ++j) s[j] = fmaf(w, __ldcg(o + j), s[j]);
-        }
-        st_v4((T*)a.y + (size_t)n * a.H + h, Vec<T>::from_float(s));
-      }
-      continue;
-    }
+    __syncthreads();
+    if (t >= n_up + n_down) break;
+    int next = 0;
+    if (tid == 0) next = atomicAdd(a.queue, 1);      // arrives during this tile
     const bool up = t < n_up;
     if (!up) t -= n_up;
     const int u = up ? t / nft : t / nht;
-    const int c0 = (up ? t % nft : t % nht) * kCols;
+    const int c0 = (up ? t % nft : t % nht) * C;
     const int e = sm.plan.expert[u], base = sm.plan.off[u], cnt = sm.plan.off[u + 1] - base;
     const size_t eo = (size_t)e * a.H * a.F;
     if (up) {
       if (tid < a.N && ((sm.plan.mask[e][tid >> 5] >> (tid & 31)) & 1u))
         sm.tokens[plan_row(sm.plan, tid, e) - base] = tid;
-      const T* const W[2] = {(const T*)a.W1 + eo, (const T*)a.W3 + eo};
-      tile<T, WIDE, 2>(
-          sm, W, a.H, a.F, c0, cnt,
-          [&](int r, int h) { return to_f<T>(x[(size_t)sm.tokens[r] * a.H + h]); },
-          [&](int r, int c, const float (&v)[2]) { act[(size_t)(base + r) * a.F + c] = from_f<T>(silu_f(v[0]) * v[1]); });
+      const float* const W[2] = {(const float*)a.W1 + eo, (const float*)a.W3 + eo};
+      tile<CT, WIDE, false, 2>(
+          a, patience, sm, W, a.H, a.F, c0, cnt, [&](int r, int h) { return __ldg(x + (size_t)sm.tokens[r] * a.H + h); },
+          [&](int r, int c, const float (&v)[2]) { st_word(act + (size_t)(base + r) * a.F + c, silu_f(v[0]) * v[1]); });
     } else {
-      if (tid == 0) sm.ok = wait_count(a.cnt->done_act + u, nft, a.cnt, a.status);
-      __syncthreads();
-      if (!sm.ok) return;
-      const T* const W[1] = {(const T*)a.W2 + eo};
-      tile<T, true, 1>(
-          sm, W, a.F, a.H, c0, cnt,
-          // past L1: another block may have left this sector there half written
-          [&](int r, int f) { return to_f<T>(__ldcg(act + (size_t)(base + r) * a.F + f)); },
-          [&](int r, int c, const float (&v)[1]) { a.out[(size_t)(base + r) * a.H + c] = v[0]; });
+      const float* const W[1] = {(const float*)a.W2 + eo};
+      tile<CT, true, true, 1>(
+          a, patience, sm, W, a.F, a.H, c0, cnt, [&](int r, int f) { return ld_word(act + (size_t)(base + r) * a.F + f); },
+          [&](int r, int c, const float (&v)[1]) { st_word(a.out + (size_t)(base + r) * a.H + c, v[0]); });
     }
+    if (tid == 0) sm.ticket = next;
     __syncthreads();
-    if (tid == 0) {
-      __threadfence();
-      add_release(up ? a.cnt->done_act + u : &a.cnt->done_down, 1);
+  }
+  // y[n] = sum_k w[n,k] out[row(n,k)], k in order; a static share, nothing waits for it
+  const Share sh = share_of(a, (int)gridDim.x);
+  for (int at = sh.v0 + tid; at < sh.v1; at += kThreads) {
+    const int n = at / sh.per_row, h = (at - n * sh.per_row) * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < a.K; k0 += 4) {            // four experts in flight
+      float4 v[4];
+      const float* o[4];
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + i;
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        w[i] = 0.f;
+        if (k < a.K) {
+          const int e = cut.here ? sm.pick.id[n][k] : __ldcg(a.top + (size_t)n * a.K + k);
+          w[i] = cut.here ? sm.pick.w[n][k] : __ldcg(a.weights + (size_t)n * a.K + k);
+          o[i] = a.out + (size_t)plan_row(sm.plan, n, e) * a.H + h;
+          v[i] = ld_words4(o[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (k0 + i >= a.K) break;
+        while (empty(v[i]) && patience.again(a.cnt, a.status)) v[i] = ld_words4(o[i]);
+        s.x = fmaf(w[i], v[i].x, s.x); s.y = fmaf(w[i], v[i].y, s.y);
+        s.z = fmaf(w[i], v[i].z, s.z); s.w = fmaf(w[i], v[i].w, s.w);
+      }
     }
+    *(float4*)((float*)a.y + (size_t)n * a.H + h) = s;
+  }
+  if (tid == 0 && atomicAdd(a.queue + 1, 1) == (int)gridDim.x - 1) {   // the last block out: ready for the next call
+    a.queue[0] = 0;
+    a.queue[1] = 0;
   }
 }
 
@@ -377,6 +431,7 @@ RouteCut route_cut(int N, int H, int E) {
   c.groups = (int)cdiv(N, c.TG);
   const int most = (int)cdiv(H, 64), want = (int)cdiv(296, c.groups);
   c.S = most < want ? most : want;
+  c.here = N <= kPickTokens && N * c.S * c.EP <= kPickFloats;
   return c;
 }
 
@@ -424,7 +479,7 @@ size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, 
     a->queue = (int*)(base + 192);
     a->cnt = (Counters*)cnt;
     a->zero_ints = (int)(zero / sizeof(int));
-    if (dt == MOE_BF16 && N <= kDirectTokens) {
+    if (dt == MOE_F32 || N <= kDirectTokens) {
       a->fill = (uint4*)act;
       a->fill_vecs = (int64_t)((off - fill0) / sizeof(uint4));
     }
@@ -465,13 +520,25 @@ moe_status route_any(const Args& a, const RouteCut& c, int pick, cudaStream_t s)
   return MOE_OK;
 }
 
-// Launched while the router still runs: it waits there for the router's end.
-template <class Kernel>
-moe_status launch_after(Kernel k, int blocks, int threads, const Args& a, cudaStream_t s, const char* name) {
+template <int CT, bool WIDE>
+moe_status experts(const Args& a, const RouteCut& cut, cudaStream_t s) {
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    if (cudaFuncSetAttribute(decode_experts_kernel<CT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(Smem)) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  // launched while the router still runs: it waits there for the router's end
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.gridDim = dim3(2 * kBlocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Smem);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -479,19 +546,18 @@ moe_status launch_after(Kernel k, int blocks, int threads, const Args& a, cudaSt
   cfg.attrs = at;
   cfg.numAttrs = 1;
   cudaError_t err = cudaSuccess;
-  MOE_TRACED(name, s, (err = cudaLaunchKernelEx(&cfg, k, a)));
+  MOE_TRACED("decode_experts", s, (err = cudaLaunchKernelEx(&cfg, decode_experts_kernel<CT, WIDE>, a, cut)));
   if (err != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }
-
-template <typename T>
-moe_status experts(const Args& a, cudaStream_t s) {
-  const int blocks = 148 * 4;
-  return a.F % Vec<T>::N == 0 ? launch_after(decode_experts_kernel<T, true>, blocks, kThreads, a, s, "decode_experts")
-                              : launch_after(decode_experts_kernel<T, false>, blocks, kThreads, a, s, "decode_experts");
+moe_status experts_any(const Args& a, const RouteCut& cut, cudaStream_t s) {
+  const int64_t used = (int64_t)a.N * a.K < a.E ? (int64_t)a.N * a.K : a.E;
+  const bool narrow = used * cdiv(a.F, 64) < 4 * kBlocks;    // 32 columns a tile where 64 leave blocks without work
+  if (a.F % 4 == 0) return narrow ? experts<8, true>(a, cut, s) : experts<16, true>(a, cut, s);
+  return narrow ? experts<8, false>(a, cut, s) : experts<16, false>(a, cut, s);
 }
 
 }  // namespace
@@ -531,10 +597,10 @@ moe_status moe_layer_decode(const void* x, const void* W_r, const void* W1, cons
   cudaStream_t s = (cudaStream_t)stream;
   const RouteCut c = route_cut(N, H, E);
   if (dt == MOE_F32) {
-    const moe_status rs = route_any<float>(a, c, 1, s);
-    return rs != MOE_OK ? rs : experts<float>(a, s);
+    const moe_status rs = route_any<float>(a, c, !c.here, s);
+    return rs != MOE_OK ? rs : experts_any(a, c, s);
   }
-  const moe_status rs = route_any<__nv_bfloat16>(a, c, N > kPickTokens, s);
+  const moe_status rs = route_any<__nv_bfloat16>(a, c, !c.here, s);
   return rs != MOE_OK ? rs : experts_umma(a, c, w.part_up, w.part_down, w.tile_cnt, s);
 }
 

@@ -12,7 +12,9 @@
 namespace moe {
 namespace decode {
 
+constexpr int kBlocks = 148;                // of the expert kernels: one an SM
 constexpr int kMaxTokens = 128;
+static_assert(kMaxTokens <= kBlocks, "a block's share of y lies in two rows");
 constexpr int kMaxExperts = 256;
 constexpr int kMaskWords = kMaxTokens / 32;
 constexpr int kMaxGroups = 32;              // token groups of the router
@@ -20,10 +22,9 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // Counters, zeroed by the router kernel of every call.
 struct Counters {
-  int ticket;                  // next unit of work (fp32)
   int abort;                   // a wait gave up: the others stop too
   int done_down;               // finished down-projection work, whole call
-  int pad;
+  int pad[2];
   int done_act[kMaxExperts];   // finished pieces of a slot's activations
 };
 
@@ -40,7 +41,7 @@ struct Args {
   // workspace
   int* status;
   int* arrive;                 // [kMaxGroups], inside the status region: zero between calls
-  int* queue;                  // bf16: next ticket and blocks that have left, zero between calls too
+  int* queue;                  // next ticket and blocks that have left, zero between calls too
   Counters* cnt;
   uint4* fill;                 // words that the router kernel sets to all ones
   int64_t fill_vecs;
@@ -55,13 +56,14 @@ struct Args {
 // logit_part[group][slice][token of the group][EP columns].
 constexpr int kRouteThreads = 256;
 constexpr int kRouteCols = 1024;     // most (token, expert) sums of a group
-// Up to this many tokens every block of the expert kernel picks the experts
-// itself from the partial logits, rather than wait for the router's last block to do it
-// and read the result: 2.6 us less of a 1-token call's 36 (2048/64/6/1408); with more
-// tokens the blocks would read more than they save.
-constexpr int kPickTokens = 2;
+// With few partial logits (kPickTokens tokens, kPickFloats values) every block of the
+// expert kernel picks the experts itself, rather than wait for the router's last block to do
+// it and read the result; with more they would read more than they save.
+constexpr int kPickTokens = 8;
+constexpr int kPickFloats = 8192;
 struct RouteCut {
   int TG, groups, S, EP;
+  bool here;           // the expert kernel picks
 };
 
 // Order of floats as unsigned numbers; NaN ranks like -infinity.
@@ -156,6 +158,56 @@ size_t umma_up_bytes(int N, int H, int E, int K, int F);     // partial sums of 
 size_t umma_down_bytes(int N, int H, int E, int K, int F);   // of the down product
 moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, float* part_down, int* tile_cnt, cudaStream_t s);
 
+// ---- values that are their own flags --------------------------------------------
+// The router kernel fills a buffer with a NaN that no sum has; readers poll the
+// words that they need.  A word holds all that a reader asks of it, so nothing else is ordered.
+constexpr uint32_t kEmpty = 0xffffffffu;
+__device__ __forceinline__ float not_empty(float v) {
+  return __float_as_uint(v) == kEmpty ? __uint_as_float(0x7fffffffu) : v;
+}
+__device__ __forceinline__ void st_word(float* p, float v) {
+  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(not_empty(v)) : "memory");
+}
+__device__ __forceinline__ float ld_word(const float* p) {
+  float v;
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_words2(const float* p) {
+  float2 v;
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_words4(const float* p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool empty(float2 v) {
+  return __float_as_uint(v.x) == kEmpty || __float_as_uint(v.y) == kEmpty;
+}
+__device__ __forceinline__ bool empty(float4 v) {
+  return __float_as_uint(v.x) == kEmpty || __float_as_uint(v.y) == kEmpty || __float_as_uint(v.z) == kEmpty ||
+         __float_as_uint(v.w) == kEmpty;
+}
+// The limit of a thread that polls words.
+struct Patience {
+  uint64_t t0 = 0;
+  uint32_t it = 0;
+  // another look: false when this thread, or another, gave up
+  __device__ __forceinline__ bool again(Counters* cnt, int* status) {
+    if ((++it & 63) != 0) return true;
+    if (*(volatile int*)&cnt->abort) return false;
+    const uint64_t now = umma::globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 <= kTimeoutNs) return true;
+    *(volatile int*)&cnt->abort = 1;
+    raise_status(status, MOE_DEVERR_TIMEOUT);
+    return false;
+  }
+};
+
 // ---- plan: which experts are used, by which tokens ---------------------------
 // Slots are the used experts in increasing id; a slot's rows are its tokens in
 // increasing order.  A token holds an expert at most once, so a bit mask a
@@ -211,6 +263,54 @@ __device__ __forceinline__ void build_plan(Plan& p, const int32_t* top, int N, i
   __syncthreads();
 }
 
+// What a block of the expert kernel picked, for cut.here.
+struct Picked {
+  int id[kPickTokens][32];
+  float w[kPickTokens][32];
+};
+template <int V>
+__device__ __forceinline__ void pick_all_v(const Args& a, const RouteCut& cut, Plan& plan, Picked& pick, float* red) {
+  constexpr int EP = 32 * V;
+  const int pass = kRouteCols / EP < kPickTokens ? kRouteCols / EP : kPickTokens;
+  for (int n0 = 0; n0 < a.N; n0 += pass) {
+    if (n0) __syncthreads();
+    pick_experts<V>(a.logit_part + (size_t)n0 * cut.S * EP, a.N - n0 < pass ? a.N - n0 : pass, (size_t)cut.S * EP,
+                    cut.S, EP, a.E, a.K, red, [&](int r, int k, int e, float w) {
+                      const int n = n0 + r;
+                      plan_add(plan, n, e);
+                      pick.id[n][k] = e;
+                      pick.w[n][k] = w;
+                      if (blockIdx.x == 0) {
+                        a.top[n * a.K + k] = e;
+                        a.weights[n * a.K + k] = w;
+                      }
+                    });
+  }
+}
+// After clear_plan; the router's groups are of one token.
+__device__ __forceinline__ void pick_all(const Args& a, const RouteCut& cut, Plan& plan, Picked& pick, float* red) {
+  switch (cut.EP) {
+    case 32: pick_all_v<1>(a, cut, plan, pick, red); break;
+    case 64: pick_all_v<2>(a, cut, plan, pick, red); break;
+    case 128: pick_all_v<4>(a, cut, plan, pick, red); break;
+    default: pick_all_v<8>(a, cut, plan, pick, red); break;
+  }
+}
+
+// A block's share of y: vectors [v0, v1) of four columns.  At most a row, so it lies in one
+// or two tokens (kMaxTokens <= kBlocks).
+struct Share {
+  int per_row, v0, v1, first;
+};
+__device__ __forceinline__ Share share_of(const Args& a, int blocks) {
+  Share h;
+  h.per_row = a.H / 4;
+  const int vecs = a.N * h.per_row, share = (vecs + blocks - 1) / blocks;
+  h.v0 = (int)blockIdx.x * share;
+  h.v1 = h.v0 + share < vecs ? h.v0 + share : vecs;
+  h.first = h.v0 / h.per_row;
+  return h;
+}
 // Row of (token n, expert e) among all rows.
 __device__ __forceinline__ int plan_row(const Plan& p, int n, int e) {
   int r = p.off[p.slot_of[e]];

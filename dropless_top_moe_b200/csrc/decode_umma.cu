@@ -45,7 +45,6 @@ namespace {
 
 using namespace umma;
 
-constexpr int kBlocks = 148;
 constexpr int kThreads = 256;
 constexpr int kBuilders = 5;                // direct variant: warp 1 and four more build token tiles
 constexpr int kDirectThreads = 384;
@@ -109,49 +108,6 @@ __device__ __forceinline__ Piece piece_at(const Line& l, int pos, int end) {
   p.len = l.kc - p.k0 < end - pos ? l.kc - p.k0 : end - pos;
   return p;
 }
-// A word that nothing has written yet (direct variant).
-constexpr uint32_t kEmpty = 0xffffffffu;
-__device__ __forceinline__ float not_empty(float v) {
-  return __float_as_uint(v) == kEmpty ? __uint_as_float(0x7fffffffu) : v;
-}
-__device__ __forceinline__ void st_word(float* p, float v) {
-  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(not_empty(v)) : "memory");
-}
-__device__ __forceinline__ float2 ld_words2(const float* p) {
-  float2 v;
-  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_words4(const float* p) {
-  float4 v;
-  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ bool empty(float2 v) {
-  return __float_as_uint(v.x) == kEmpty || __float_as_uint(v.y) == kEmpty;
-}
-__device__ __forceinline__ bool empty(float4 v) {
-  return __float_as_uint(v.x) == kEmpty || __float_as_uint(v.y) == kEmpty || __float_as_uint(v.z) == kEmpty ||
-         __float_as_uint(v.w) == kEmpty;
-}
-// The limit of a thread that polls words.
-struct Patience {
-  uint64_t t0 = 0;
-  uint32_t it = 0;
-  // another look: false when this thread, or another, gave up
-  __device__ __forceinline__ bool again(Counters* cnt, int* status) {
-    if ((++it & 63) != 0) return true;
-    if (*(volatile int*)&cnt->abort) return false;
-    const uint64_t now = globaltimer();
-    if (t0 == 0) t0 = now;
-    if (now - t0 <= kTimeoutNs) return true;
-    *(volatile int*)&cnt->abort = 1;
-    raise_status(status, MOE_DEVERR_TIMEOUT);
-    return false;
-  }
-};
-
 struct Ticket {
   bool up, stop;
   int t;
@@ -196,38 +152,21 @@ struct Shared {
   int last;
   int ok;
   float4 sum[kThreads];
-  int pick_id[kPickTokens][32];
-  float pick_w[kPickTokens][32];
+  Picked pick;
   // of the one or two tokens whose columns this block adds up
   float w[2][32];
   int row[2][32], tile[2][32], row0[2][32];
 };
-static_assert(kMaxTokens <= kBlocks, "a block's share of y is at most a row, so it lies in two");
 static_assert(kThreads == kRouteThreads, "pick_experts");
 
-// A block's share of y: vectors [v0, v1) of four columns, and the routing of the
-// one or two tokens that they belong to.
-struct Share {
-  int per_row, v0, v1, first;
-};
-__device__ __forceinline__ Share share_of(const Args& a) {
-  Share h;
-  h.per_row = a.H / 4;
-  const int vecs = a.N * h.per_row, share = (vecs + kBlocks - 1) / kBlocks;
-  h.v0 = (int)blockIdx.x * share;
-  h.v1 = h.v0 + share < vecs ? h.v0 + share : vecs;
-  h.first = h.v0 / h.per_row;
-  return h;
-}
 // Thread i of 2 K: expert i % K of the share's token i / K.
-__device__ __forceinline__ void prepare_sum(const Args& a, Shared& sm, const Line& down, int i) {
-  const Share h = share_of(a);
+__device__ __forceinline__ void prepare_sum(const Args& a, Shared& sm, const Line& down, bool here, int i) {
+  const Share h = share_of(a, kBlocks);
   const int ti = i / a.K, k = i - ti * a.K, n = h.first + ti;
   if (h.v0 >= h.v1 || n >= a.N) return;
-  const bool here = a.N <= kPickTokens;
-  const int e = here ? sm.pick_id[n][k] : __ldcg(a.top + n * a.K + k);
+  const int e = here ? sm.pick.id[n][k] : __ldcg(a.top + n * a.K + k);
   const int u = sm.plan.slot_of[e];
-  sm.w[ti][k] = here ? sm.pick_w[n][k] : __ldcg(a.weights + n * a.K + k);
+  sm.w[ti][k] = here ? sm.pick.w[n][k] : __ldcg(a.weights + n * a.K + k);
   sm.row[ti][k] = plan_row(sm.plan, n, e);
   sm.row0[ti][k] = sm.plan.off[u];
   sm.tile[ti][k] = u * down.nj;
@@ -243,7 +182,7 @@ template <bool DIRECT>
 __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const Line& down) {
   const Args& a = p.a;
   const int tid = threadIdx.x;
-  const Share sh = share_of(a);
+  const Share sh = share_of(a, kBlocks);
   const int per_row = sh.per_row, v0 = sh.v0, v1 = sh.v1, share = v1 - v0, first = sh.first;
   if (v0 >= v1) return;
   int KL = 1;
@@ -305,23 +244,6 @@ __device__ __forceinline__ void weighted_sums(const Params& p, Shared& sm, const
   }
 }
 
-// The experts of up to kPickTokens tokens, from the router's groups of one token.
-template <int V>
-__device__ __forceinline__ void pick_here(const Params& p, Shared& sm, float* red) {
-  static_assert(kPickTokens * 32 * V <= kRouteCols, "one pass");
-  const Args& a = p.a;
-  const int S = p.cut.S, EP = 32 * V;
-  pick_experts<V>(a.logit_part, a.N, (size_t)S * EP, S, EP, a.E, a.K, red, [&](int n, int k, int e, float w) {
-    plan_add(sm.plan, n, e);
-    sm.pick_id[n][k] = e;
-    sm.pick_w[n][k] = w;
-    if (blockIdx.x == 0) {
-      a.top[n * a.K + k] = e;
-      a.weights[n * a.K + k] = w;
-    }
-  });
-}
-
 template <bool DIRECT>
 __global__ void __launch_bounds__(DIRECT ? kDirectThreads : kThreads, 1)
 decode_umma_kernel(const __grid_constant__ Params p) {
@@ -365,14 +287,9 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   if (tid == 0) v = atomicAdd(a.queue, 1);
   clear_plan(sm.plan, (int)blockDim.x);
   pdl_wait();
-  if (a.N <= kPickTokens) {
+  if (p.cut.here) {
     float* red = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));   // the ring is still empty
-    switch (p.cut.EP) {
-      case 32: pick_here<1>(p, sm, red); break;
-      case 64: pick_here<2>(p, sm, red); break;
-      case 128: pick_here<4>(p, sm, red); break;
-      default: pick_here<8>(p, sm, red); break;
-    }
+    pick_all(a, p.cut, sm.plan, sm.pick, red);
     build_plan(sm.plan, nullptr, a.N, a.K, a.E, (int)blockDim.x);
     fence_proxy_async();       // `red` was written where TMA will write
   } else {
@@ -386,7 +303,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   const Line down = make_line(sm.plan.slots, (a.H + 255) / 256, a.F / kKB, kDownTickets);
 
   if (warp == (DIRECT ? kDirectThreads / 32 - 1 : 4))
-    for (int i = lane; i < 2 * a.K; i += 32) prepare_sum(a, sm, down, i);
+    for (int i = lane; i < 2 * a.K; i += 32) prepare_sum(a, sm, down, p.cut.here, i);
 
   // the roles' view of the ticket ring
   int slot = 0;
