@@ -428,22 +428,18 @@ RouteCut route_cut(int N, int H, int E) {
   c.EP = 32;
   while (c.EP < E) c.EP *= 2;
   c.TG = N <= 8 ? 1 : (N <= 32 ? 2 : 4);
-  c.groups = (int)cdiv(N, c.TG);
+  c.groups = N > 0 ? (int)cdiv(N, c.TG) : 1;
   const int most = (int)cdiv(H, 64), want = (int)cdiv(296, c.groups);
   c.S = most < want ? most : want;
   c.here = N <= kPickTokens && N * c.S * c.EP <= kPickFloats;
   return c;
 }
 
+// Room for the cut of any token count up to N: groups * S * TG rows of EP, and
+// groups * S < 296 + groups, groups * TG < N + TG, S <= ceil(H / 64).
 size_t part_bytes(int N, int H, int E) {
-  // the largest cut of any token count up to N
-  size_t most = 0;
-  for (int n = 1; n <= N; ++n) {
-    const RouteCut c = route_cut(n, H, E);
-    const size_t b = (size_t)c.groups * c.S * c.TG * c.EP * sizeof(float);
-    if (b > most) most = b;
-  }
-  return most;
+  const int64_t few = round_up(N, 4) * cdiv(H, 64), most = 4 * 296 + N + 4;
+  return (size_t)(few < most ? few : most) * route_cut(N, H, E).EP * sizeof(float);
 }
 
 // What only the bf16 expert kernel has.

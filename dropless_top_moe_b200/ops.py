@@ -247,28 +247,34 @@ def moe_aux_loss(probs, bins, K: int, alpha: float, ws=None):
     return loss, P
 
 
-def _same_device(named) -> torch.device:
-    """The CUDA device every given tensor lives on."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name}: tensors must live on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
-    return dev
+def _arg(name: str, t: torch.Tensor, shape, dtype, dev: Optional[int]):
+    """Pointer of an argument, after the checks of _check and _p; dev: index of the device it has to be on.
+    One pass, since small calls are bound by the host."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensors must live on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the other tensors on cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _call_on(dev: torch.device, name: str, *args) -> None:
-    """Call an entry point on `dev` and its current stream, whichever device is current."""
-    if dev.index == torch.cuda.current_device():
-        call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+# the current stream's handle, without a Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call_on(dev: int, name: str, *args) -> None:
+    """Call an entry point on device `dev` and its current stream, whichever device is current."""
+    if dev == torch.cuda.current_device():
+        call(name, *args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+            call(name, *args, _raw_stream(dev))
 
 
 def moe_add_rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None):
@@ -277,49 +283,52 @@ def moe_add_rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None
     x, residual [N, H], weight [H].  y and h may be given, also to work in place
     (h = residual or x, y = x or residual, two different buffers).
     """
-    if x.dim() != 2:
-        raise ValueError(f"x: expected [N, H], got {tuple(x.shape)}")
-    N, H = x.shape
-    dt = _dt(x)
-    _check("weight", weight, (H,), x.dtype)
-    _check("residual", residual, (N, H), x.dtype)
-    _check("y", y, (N, H), x.dtype)
-    _check("h", h, (N, H), x.dtype)
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    if len(shape) != 2:
+        raise ValueError(f"x: expected [N, H], got {tuple(shape)}")
     if h is not None and residual is None:
         raise ValueError("h: without a residual h is x itself")
-    dev = _same_device((("x", x), ("weight", weight), ("residual", residual), ("y", y), ("h", h)))
+    N, H = shape
+    dt = _dt(x)
+    pw = _arg("weight", weight, (H,), dtype, dev) if x.is_cuda else _check("weight", weight, (H,), dtype)
+    if residual is not None and not x.is_cuda:
+        _check("residual", residual, shape, dtype)
+    px = _arg("x", x, shape, dtype, dev)
+    pr = ph = None
     if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if residual is not None and h is None:
-        h = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if h is not None and N > 0 and h.data_ptr() == y.data_ptr():
-        raise ValueError("y and h must be different buffers")
-    _call_on(dev, "moe_add_rms_norm", _p(x), _p(residual), _p(weight), N, H, dt, float(eps), _p(h), _p(y))
+        y = torch.empty_like(x)
+    if residual is not None:
+        pr = _arg("residual", residual, shape, dtype, dev)
+        if h is None:
+            h = torch.empty_like(x)
+        ph = _arg("h", h, shape, dtype, dev)
+    _call_on(dev, "moe_add_rms_norm", px, pr, pw, N, H, dt, eps, ph, _arg("y", y, shape, dtype, dev))
     return y, (x if residual is None else h)
 
 
 def moe_add_rms_norm_bwd(dy, h, weight, dh=None, eps: float = 1e-6, dx=None, dweight=None, ws=None):
     """Gradients of moe_add_rms_norm: (dx, dweight).  h is the forward's; dh is the gradient
     that reaches h past the norm.  dx is the gradient of x and of residual alike."""
-    if dy.dim() != 2:
-        raise ValueError(f"dy: expected [N, H], got {tuple(dy.shape)}")
-    N, H = dy.shape
+    shape, dtype, dev = dy.shape, dy.dtype, dy.get_device()
+    if len(shape) != 2:
+        raise ValueError(f"dy: expected [N, H], got {tuple(shape)}")
+    N, H = shape
     dt = _dt(dy)
-    _check("h", h, (N, H), dy.dtype)
-    _check("weight", weight, (H,), dy.dtype)
-    _check("dh", dh, (N, H), dy.dtype)
-    _check("dx", dx, (N, H), dy.dtype)
-    _check("dweight", dweight, (H,), dy.dtype)
-    dev = _same_device((("dy", dy), ("h", h), ("weight", weight), ("dh", dh), ("dx", dx), ("dweight", dweight),
-                        ("ws", ws)))
+    if not dy.is_cuda:
+        for name, t, want in (("h", h, shape), ("weight", weight, (H,)), ("dh", dh, shape), ("dx", dx, shape),
+                              ("dweight", dweight, (H,))):
+            _check(name, t, want, dtype)
+    pdy = _arg("dy", dy, shape, dtype, dev)
     if dx is None:
-        dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
+        dx = torch.empty_like(dy)
     if dweight is None:
-        dweight = torch.empty(H, dtype=dy.dtype, device=dev)
+        dweight = torch.empty_like(weight)
     if ws is None:
-        ws = torch.empty(load().moe_add_rms_norm_bwd_workspace_size(N, H, dt), dtype=torch.uint8, device=dev)
-    _call_on(dev, "moe_add_rms_norm_bwd", _p(dy), _p(h), _p(weight), _p(dh), N, H, dt, float(eps), _p(dx),
-             _p(dweight), _p(ws), ws.numel())
+        ws = torch.empty(load().moe_add_rms_norm_bwd_workspace_size(N, H, dt), dtype=torch.uint8, device=dy.device)
+    _call_on(dev, "moe_add_rms_norm_bwd", pdy, _arg("h", h, shape, dtype, dev), _arg("weight", weight, (H,), dtype, dev),
+             None if dh is None else _arg("dh", dh, shape, dtype, dev), N, H, dt, eps,
+             _arg("dx", dx, shape, dtype, dev), _arg("dweight", dweight, (H,), dtype, dev),
+             _arg("ws", ws, (ws.numel(),), torch.uint8, dev), ws.numel())
     return dx, dweight
 
 
@@ -343,27 +352,30 @@ def moe_clip_grad_norm(grads, max_norm: float, outs=None, ws=None, norm=None) ->
         outs = list(outs)
         if len(outs) != n:
             raise ValueError(f"outs: expected {n} tensors, got {len(outs)}")
-    _check("norm", norm, (1,), torch.float32)
-    ptrs, sizes, dts = [], [], []
-    for i, g in enumerate(grads):
-        dts.append(_dt(g))
-        sizes.append(g.numel())
-        if outs is not None:
-            _check(f"outs[{i}]", outs[i], tuple(g.shape), g.dtype)
-    dev = _same_device([("grads", g) for g in grads] + [("outs", o) for o in outs or ()] +
-                       [("ws", ws), ("norm", norm)])
-    if dev is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
-    ptrs = [_p(g) for g in grads]
-    outp = [_p(o) for o in outs] if outs is not None else None
+    named = grads[0] if n else (ws if ws is not None else norm)
+    dev = named.get_device() if named is not None else torch.cuda.current_device()
+    dts = [_dt(g) for g in grads]
+    if outs is not None and n and not grads[0].is_cuda:
+        for i, (o, g) in enumerate(zip(outs, grads)):
+            _check(f"outs[{i}]", o, g.shape, g.dtype)
+    if norm is not None:
+        _check("norm", norm, (1,), torch.float32)
+    ptrs = [_arg("grads", g, g.shape, g.dtype, dev) for g in grads]
+    outp = None
+    if outs is not None:
+        outp = [_arg(f"outs[{i}]", o, g.shape, g.dtype, dev) for i, (o, g) in enumerate(zip(outs, grads))]
     if ws is None:
-        ws = torch.empty(load().moe_clip_grad_norm_workspace_size(n), dtype=torch.uint8, device=dev)
+        ws = torch.empty(load().moe_clip_grad_norm_workspace_size(n), dtype=torch.uint8, device=f"cuda:{dev}")
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
-    _call_on(dev, "moe_clip_grad_norm", (ctypes.c_void_p * n)(*ptrs) if n else None,
-             (ctypes.c_void_p * n)(*outp) if n and outp is not None else None,
-             (ctypes.c_int64 * n)(*sizes) if n else None, (ctypes.c_int32 * n)(*dts) if n else None,
-             n, float(max_norm), _p(norm), _p(ws), ws.numel())
+        norm = torch.empty(1, dtype=torch.float32, device=f"cuda:{dev}")
+    if n:
+        P = ctypes.c_void_p * n
+        lists = (P(*ptrs), None if outp is None else P(*outp), (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
+                 (ctypes.c_int32 * n)(*dts))
+    else:
+        lists = (None, None, None, None)
+    _call_on(dev, "moe_clip_grad_norm", *lists, n, max_norm, _arg("norm", norm, (1,), torch.float32, dev),
+             _arg("ws", ws, (ws.numel(),), torch.uint8, dev), ws.numel())
     return norm
 
 
@@ -486,27 +498,25 @@ class MoEDecodeLayer:
         self.y = torch.empty(N, H, dtype=dtype, device=dev)
         self._top = torch.empty(N, K, dtype=torch.int32, device=dev)
         self._weights = torch.empty(N, K, dtype=torch.float32, device=dev)
-        self.top_experts, self.weights = self._top, self._weights
+        self.top_experts, self.weights, self._y = self._top, self._weights, self.y   # of the last call's n rows
+        self._n = N
+        self._ptrs = (self._top.data_ptr(), self._weights.data_ptr(), self.ws.data_ptr(), self.ws.numel())
 
     def forward(self, x, W_r, W1, W3, W2, y=None):
-        H, E, F, dt = self.H, self.E, self.F, self.dtype
+        H, E, F, dt, dev = self.H, self.E, self.F, self.dtype, self.device.index
         if x.dim() != 2 or x.shape[0] > self.N:
             raise ValueError(f"x: expected at most {self.N} rows of {H}, got {tuple(x.shape)}")
         n = x.shape[0]
-        _check("x", x, (n, H), dt)
-        _check("W_r", W_r, (H, E), dt)
-        _check("W1", W1, (E, H, F), dt)
-        _check("W3", W3, (E, H, F), dt)
-        _check("W2", W2, (E, F, H), dt)
-        _check("y", y, (n, H), dt)
-        for name, t in (("x", x), ("W_r", W_r), ("W1", W1), ("W3", W3), ("W2", W2), ("y", y)):
-            if t is not None and t.device != self.device:
-                raise ValueError(f"{name}: on {t.device}, the layer on {self.device}")
+        if n != self._n:
+            self._n, self._y = n, self.y[:n]
+            self.top_experts, self.weights = self._top[:n], self._weights[:n]
         if y is None:
-            y = self.y[:n]
-        self.top_experts, self.weights = self._top[:n], self._weights[:n]
-        _call_on(self.device, "moe_layer_decode", _p(x), _p(W_r), _p(W1), _p(W3), _p(W2), n, H, E, self.K, F, self.dt,
-                 _p(y), self._top.data_ptr(), self._weights.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+            y = self._y
+        top, weights, ws, ws_bytes = self._ptrs
+        _call_on(dev, "moe_layer_decode", _arg("x", x, (n, H), dt, dev), _arg("W_r", W_r, (H, E), dt, dev),
+                 _arg("W1", W1, (E, H, F), dt, dev), _arg("W3", W3, (E, H, F), dt, dev),
+                 _arg("W2", W2, (E, F, H), dt, dev), n, H, E, self.K, F, self.dt, _arg("y", y, (n, H), dt, dev), top,
+                 weights, ws, ws_bytes)
         return y
 
     def status(self) -> int:
