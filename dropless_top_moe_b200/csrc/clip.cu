@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 namespace {
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kClipThreads)
 grad_squares_kernel(const __grid_constant__ ClipTable<M> tab, double* __restrict__ part) {
   __shared__ double red[kClipThreads / 32];
   double sum = 0.0;
+  pdl_launch();
   for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
     const int i = tensor_of(tab, c);
     const ClipTensor& t = tab.t[i];
@@ -189,6 +191,7 @@ grad_scale_kernel(const __grid_constant__ ClipTable<M> tab, const double* __rest
                   float max_norm, int copy, float* norm_out) {
   __shared__ double red[kClipThreads / 32];
   double sum = 0.0;
+  pdl_wait();
   for (int i = threadIdx.x; i < n_part; i += kClipThreads) sum += part[i];
   const double norm = sqrt(block_sum_f64(sum, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
@@ -278,9 +281,14 @@ moe_status clip_run(const void* const* grads, void* const* outs, const int64_t* 
           n_part += blocks;
         }
       } else if (blocks > 0 || first) {
-        MOE_TRACED("grad_scale", s, (grad_scale_kernel<M><<<blocks > 0 ? blocks : 1, kClipThreads, 0, s>>>(
-                                        tab, part, n_part, max_norm, copy ? 1 : 0, first ? norm : nullptr)));
-        MOE_LAUNCH_CHECK();
+        cudaError_t err = cudaSuccess;
+        MOE_TRACED("grad_scale", s,
+                   (err = launch_after(grad_scale_kernel<M>, blocks > 0 ? blocks : 1, kClipThreads, 0, s, tab, part, n_part,
+                                       max_norm, copy ? 1 : 0, first ? norm : nullptr)));
+        if (err != cudaSuccess) {
+          (void)cudaGetLastError();
+          return MOE_ERR_CUDA;
+        }
       }
       first = false;
     }

@@ -529,20 +529,9 @@ moe_status experts(const Args& a, const RouteCut& cut, cudaStream_t s) {
     }
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  // launched while the router still runs: it waits there for the router's end
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(2 * kBlocks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Smem);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   cudaError_t err = cudaSuccess;
-  MOE_TRACED("decode_experts", s, (err = cudaLaunchKernelEx(&cfg, decode_experts_kernel<CT, WIDE>, a, cut)));
+  MOE_TRACED("decode_experts", s, (err = launch_after(decode_experts_kernel<CT, WIDE>, 2 * kBlocks, kThreads, sizeof(Smem),
+                                                      s, a, cut)));
   if (err != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;

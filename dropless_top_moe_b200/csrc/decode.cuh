@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "pdl.cuh"
 #include "umma.cuh"
 
 #include <math.h>
@@ -354,9 +355,6 @@ __device__ __forceinline__ bool wait_count(const int* p, int want, Counters* cnt
     }
   }
 }
-
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace decode
 }  // namespace moe

@@ -780,22 +780,12 @@ moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, floa
     }
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(kBlocks);
-  cfg.blockDim = dim3(a.N <= kDirectTokens ? kDirectThreads : kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   cudaError_t err = cudaSuccess;
   if (a.N <= kDirectTokens)
-    MOE_TRACED("decode_experts_direct", s, (err = cudaLaunchKernelEx(&cfg, decode_umma_kernel<true>, p)));
+    MOE_TRACED("decode_experts_direct", s,
+               (err = launch_after(decode_umma_kernel<true>, kBlocks, kDirectThreads, smem, s, p)));
   else
-    MOE_TRACED("decode_experts_umma", s, (err = cudaLaunchKernelEx(&cfg, decode_umma_kernel<false>, p)));
+    MOE_TRACED("decode_experts_umma", s, (err = launch_after(decode_umma_kernel<false>, kBlocks, kThreads, smem, s, p)));
   if (err != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;

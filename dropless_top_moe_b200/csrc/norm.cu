@@ -10,14 +10,19 @@
 // stays in fp32 and is rounded once, at the store.
 //
 // Both directions do a few operations per byte, so HBM bounds them: four
-// elements of N * H moved either way.  A block owns one row at a time and keeps it in
-// registers (16-byte loads, VPT vectors a thread), so each element is read
-// once; the next row's loads are issued before this row's reduction, which
-// keeps loads in flight across the barrier.  The backward accumulates its rows' dw in
-// registers; each block then writes one partial row and a second kernel sums the
-// partials in block order, so dw has the same bits on every run.
+// elements of N * H moved either way.  A block owns one row at a time, holds it in
+// registers (VPT 16-byte vectors a thread) and so reads each element once.  The rows to
+// come are on their way meanwhile: every thread copies its own vectors of the next
+// rows to shared memory (cp.async), one or two rows ahead, and reads only what it
+// copied itself, so this costs neither registers nor barriers; one barrier a row
+// remains, in the row's sum.  The backward accumulates its rows' dw in registers; each
+// block then writes one partial row and a second kernel sums the partials in
+// block order, so dw has the same bits on every run.
+#include <string.h>
+
 #include "common.cuh"
 #include "kernels.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 namespace {
@@ -26,13 +31,61 @@ constexpr int kNormSms = 148;      // blocks are a multiple of this (fixed: dw m
 constexpr int kNormMaxVec = 512 * 4;   // 16-byte vectors of a row: 512 threads, 4 each
 constexpr int kDwCols = 32, kDwRows = 16;   // block of the dw reduction
 
-// Streamed once: not kept in L1.
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-  return r;
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// This thread's vectors of the rows to come: each of D slots holds NIN operands' VPT vectors.
+template <typename T, int VPT, int NIN, int D>
+struct Rows {
+  const T* src[NIN];
+  uint4* mine;        // [slot][operand][vector][thread]
+  int N, H, nv, slot;
+  __device__ __forceinline__ uint4* at(int s, int o, int i) const {
+    return mine + ((s * NIN + o) * VPT + i) * blockDim.x;
+  }
+  __device__ __forceinline__ void ask(int s, int n) {
+    if (n < N) {
+#pragma unroll
+      for (int o = 0; o < NIN; ++o)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int c = threadIdx.x + i * blockDim.x;
+          if (c < nv) copy16(at(s, o, i), src[o] + (size_t)n * H + (size_t)c * Vec<T>::N);
+        }
+    }
+    copy_commit();      // an empty group past the last row keeps the count
+  }
+  __device__ __forceinline__ static int after(int n, int N) {
+    return n < N - (int)gridDim.x ? n + (int)gridDim.x : N;
+  }
+  // The first D - 1 rows; returns the row after them.
+  __device__ __forceinline__ int begin(int n) {
+#pragma unroll
+    for (int s = 0; s < D - 1; ++s) {
+      ask(s, n);
+      if (n < N) n = after(n, N);
+    }
+    slot = 0;
+    return n;
+  }
+  // The current row's vectors, and row `ahead` asked for into the slot read last.
+  __device__ __forceinline__ void take(int ahead, uint4 (&v)[NIN][VPT]) {
+    // the oldest of D - 1 groups has arrived
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
+    ask(slot == 0 ? D - 1 : slot - 1, ahead);
+#pragma unroll
+    for (int o = 0; o < NIN; ++o)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        v[o][i] = c < nv ? *at(slot, o, i) : make_uint4(0, 0, 0, 0);
+      }
+    slot = slot == D - 1 ? 0 : slot + 1;
+  }
+};
 
 // Sum of NV values a thread over the block, in a fixed order, on every thread.
 // `red` alternates between two buffers from call to call: one barrier a call.
@@ -52,56 +105,49 @@ __device__ __forceinline__ void block_sum(float (&v)[NV], float* red) {
   for (int i = 0; i < NV; ++i) v[i] = warp_sum(lane < nw ? red[i * 32 + lane] : 0.f);
 }
 
-template <typename T, int VPT, bool RES>
+template <typename T, int VPT, int D, bool RES>
 __global__ void __launch_bounds__(512)
 add_rms_norm_kernel(const T* x, const T* residual, const T* __restrict__ weight, int N, int H, float eps,
                     T* h, T* y) {
-  constexpr int V = Vec<T>::N;
+  constexpr int V = Vec<T>::N, NIN = RES ? 2 : 1;
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float red[2][32];
   const int nv = H / V;
-  uint4 w[VPT], a[VPT], b[VPT];
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  auto load = [&](int n) {
-    const size_t row = (size_t)n * H;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      a[i] = b[i] = zero;
-      if (n < N && c < nv) {
-        a[i] = ld_stream(x + row + (size_t)c * V);
-        if (RES) b[i] = ld_stream(residual + row + (size_t)c * V);
-      }
-    }
-  };
-  load(blockIdx.x);
+  Rows<T, VPT, NIN, D> rows;
+  rows.src[0] = x;
+  if constexpr (RES) rows.src[1] = residual;
+  rows.mine = ring + threadIdx.x;
+  rows.N = N; rows.H = H; rows.nv = nv;
+  int ahead = rows.begin(blockIdx.x);
+  uint4 w[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
-    w[i] = c < nv ? ld_nc_v4(weight + (size_t)c * V) : zero;
+    w[i] = c < nv ? ld_nc_v4(weight + (size_t)c * V) : make_uint4(0, 0, 0, 0);
   }
   int buf = 0;
   for (int n = blockIdx.x, next; n < N; n = next) {
-    next = n < N - (int)gridDim.x ? n + (int)gridDim.x : N;
+    next = rows.after(n, N);
     const size_t row = (size_t)n * H;
-    uint4 hv[VPT];
+    uint4 v[NIN][VPT];
+    rows.take(ahead, v);
+    if (ahead < N) ahead = rows.after(ahead, N);
     float ss[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       float f[V];
-      hv[i] = a[i];
-      Vec<T>::to_float(a[i], f);
-      if (RES) {
+      Vec<T>::to_float(v[0][i], f);
+      if constexpr (RES) {
         float g[V];
-        Vec<T>::to_float(b[i], g);
+        Vec<T>::to_float(v[1][i], g);
 #pragma unroll
         for (int j = 0; j < V; ++j) f[j] += g[j];
-        hv[i] = Vec<T>::from_float(f);      // the residual stream is kept in T
-        Vec<T>::to_float(hv[i], f);
+        v[0][i] = Vec<T>::from_float(f);      // the residual stream is kept in T
+        Vec<T>::to_float(v[0][i], f);
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) ss[0] = fmaf(f[j], f[j], ss[0]);
     }
-    load(next);
     block_sum<1>(ss, red[buf]);
     buf ^= 1;
     const float s = 1.0f / sqrtf(ss[0] / (float)H + eps);
@@ -110,63 +156,54 @@ add_rms_norm_kernel(const T* x, const T* residual, const T* __restrict__ weight,
       const int c = threadIdx.x + i * blockDim.x;
       if (c >= nv) continue;
       float f[V], g[V];
-      Vec<T>::to_float(hv[i], f);
+      Vec<T>::to_float(v[0][i], f);
       Vec<T>::to_float(w[i], g);
 #pragma unroll
       for (int j = 0; j < V; ++j) f[j] = f[j] * s * g[j];
-      if (RES) st_v4(h + row + (size_t)c * V, hv[i]);
+      if (RES) st_v4(h + row + (size_t)c * V, v[0][i]);
       st_v4(y + row + (size_t)c * V, Vec<T>::from_float(f));
     }
   }
 }
 
-template <typename T, int VPT, bool DH>
-__global__ void __launch_bounds__(512, 1)
+template <typename T, int VPT, int D, bool DH>
+__global__ void __launch_bounds__(512)
 add_rms_norm_bwd_kernel(const T* dy, const T* h, const T* __restrict__ weight, const T* dh, int N, int H,
                         float eps, T* dx, float* __restrict__ dw_part, T* __restrict__ dw) {
-  constexpr int V = Vec<T>::N;
+  constexpr int V = Vec<T>::N, NIN = DH ? 3 : 2;
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float red[2][64];
+  pdl_launch();
   const int nv = H / V;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 w[VPT], a[VPT], b[VPT], d[VPT];
+  Rows<T, VPT, NIN, D> rows;
+  rows.src[0] = h;
+  rows.src[1] = dy;
+  if constexpr (DH) rows.src[2] = dh;
+  rows.mine = ring + threadIdx.x;
+  rows.N = N; rows.H = H; rows.nv = nv;
+  int ahead = rows.begin(blockIdx.x);
+  uint4 w[VPT];
   float acc[VPT][V];
-  auto load = [&](int n) {
-    const size_t row = (size_t)n * H;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      a[i] = b[i] = d[i] = zero;
-      if (n < N && c < nv) {
-        a[i] = ld_stream(h + row + (size_t)c * V);
-        b[i] = ld_stream(dy + row + (size_t)c * V);
-        if (DH) d[i] = ld_stream(dh + row + (size_t)c * V);
-      }
-    }
-  };
-  constexpr bool kAhead = VPT < 4;     // four vectors of three rows leave no registers for the next row's
-  if (kAhead) load(blockIdx.x);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
-    w[i] = c < nv ? ld_nc_v4(weight + (size_t)c * V) : zero;
+    w[i] = c < nv ? ld_nc_v4(weight + (size_t)c * V) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[i][j] = 0.f;
   }
   int buf = 0;
   for (int n = blockIdx.x, next; n < N; n = next) {
-    next = n < N - (int)gridDim.x ? n + (int)gridDim.x : N;
+    next = rows.after(n, N);
     const size_t row = (size_t)n * H;
-    uint4 hv[VPT], gv[VPT], dv[VPT];
-    if (!kAhead) load(n);
+    uint4 v[NIN][VPT];
+    rows.take(ahead, v);
+    if (ahead < N) ahead = rows.after(ahead, N);
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      hv[i] = a[i];
-      gv[i] = b[i];
-      dv[i] = d[i];
       float f[V], g[V], wf[V];
-      Vec<T>::to_float(hv[i], f);
-      Vec<T>::to_float(gv[i], g);
+      Vec<T>::to_float(v[0][i], f);
+      Vec<T>::to_float(v[1][i], g);
       Vec<T>::to_float(w[i], wf);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -174,7 +211,6 @@ add_rms_norm_bwd_kernel(const T* dy, const T* h, const T* __restrict__ weight, c
         sum[1] = fmaf(g[j] * wf[j], f[j], sum[1]);
       }
     }
-    if (kAhead) load(next);
     block_sum<2>(sum, red[buf]);
     buf ^= 1;
     const float s = 1.0f / sqrtf(sum[0] / (float)H + eps);
@@ -184,10 +220,10 @@ add_rms_norm_bwd_kernel(const T* dy, const T* h, const T* __restrict__ weight, c
       const int c = threadIdx.x + i * blockDim.x;
       if (c >= nv) continue;
       float f[V], g[V], wf[V], r[V];
-      Vec<T>::to_float(hv[i], f);
-      Vec<T>::to_float(gv[i], g);
+      Vec<T>::to_float(v[0][i], f);
+      Vec<T>::to_float(v[1][i], g);
       Vec<T>::to_float(w[i], wf);
-      Vec<T>::to_float(dv[i], r);
+      if constexpr (DH) Vec<T>::to_float(v[2][i], r);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float xhat = f[j] * s;
@@ -221,6 +257,7 @@ rms_norm_dw_kernel(const float* __restrict__ part, int G, int H, T* __restrict__
   const int tc = threadIdx.x % kDwCols, tr = threadIdx.x / kDwCols;
   const int c = blockIdx.x * kDwCols + tc;
   float s = 0.f;
+  pdl_wait();
   if (c < H) {
 #pragma unroll 8
     for (int g = tr; g < G; g += kDwRows) s += part[(size_t)g * H + c];
@@ -235,29 +272,34 @@ rms_norm_dw_kernel(const float* __restrict__ part, int G, int H, T* __restrict__
   }
 }
 
-// Threads of a row's block and vectors a thread: the fewest vectors (1, 2, 4)
-// that keep the block within `cap` threads.
+// Threads of a row's block, vectors a thread, rows under way, blocks.  Two vectors a
+// thread where the row allows; as many blocks an SM as kSmThreads and shared memory
+// allow; two rows ahead for the backward and for rows that leave one block an SM, one
+// row for the forward's others.  More under way was slower on long rows (16384 x 4096
+// bf16: forward 87 us, 95 with two rows ahead, 97 with twice the threads; backward
+// 83 us, 87 with one row ahead, 103 with three blocks an SM).
+constexpr int kSmThreads = 512, kSmBytes = 220 * 1024;
 struct NormShape {
-  int threads, vpt;
+  int threads, vpt, depth, blocks;
+  size_t smem;
 };
-NormShape norm_shape(int nv, int cap) {
+NormShape norm_shape(int N, int H, moe_dtype dt, int nin, bool bwd) {
+  const int nv = H / (dt == MOE_F32 ? 4 : 8);
+  const int cap = nv > 512 ? 512 : (nv > 256 ? 256 : 128);
   NormShape s;
   s.vpt = 1;
   while (s.vpt < 4 && nv > cap * s.vpt) s.vpt *= 2;
   s.threads = (int)round_up(cdiv(nv, s.vpt), 32);
+  int per_sm = kSmThreads / s.threads;
+  const size_t row = (size_t)nin * s.vpt * s.threads * 16;
+  s.depth = bwd || per_sm == 1 || nv <= 256 ? 3 : 2;
+  if (s.depth * row > kSmBytes) s.depth = 2;
+  s.smem = s.depth * row;
+  if (per_sm * s.smem > kSmBytes) per_sm = (int)(kSmBytes / s.smem);
+  const int64_t g = (int64_t)kNormSms * per_sm;
+  s.blocks = (int)(N < g ? N : g);
   return s;
 }
-
-int norm_blocks(int N, int threads, int most_threads) {
-  int per_sm = most_threads / threads;
-  if (per_sm < 1) per_sm = 1;
-  if (per_sm > 16) per_sm = 16;
-  const int64_t g = (int64_t)kNormSms * per_sm;
-  return (int)(N < g ? N : g);
-}
-
-constexpr int kFwdCap = 256, kFwdThreads = 1024;   // threads of a block before rows take more vectors; of an SM
-constexpr int kBwdCap = 256, kBwdThreads = 512;
 
 moe_status norm_check(int N, int H, moe_dtype dt) {
   if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_INVALID_ARG;
@@ -268,65 +310,81 @@ moe_status norm_check(int N, int H, moe_dtype dt) {
   return MOE_OK;
 }
 
-NormShape shape_of(int H, moe_dtype dt, int cap) {
-  const int nv = H / (dt == MOE_F32 ? 4 : 8);
-  return norm_shape(nv, nv > cap * 2 ? 512 : cap);
-}
-
 size_t bwd_partials(int N, int H, moe_dtype dt) {
-  const int G = norm_blocks(N, shape_of(H, dt, kBwdCap).threads, kBwdThreads);
+  const int a = norm_shape(N, H, dt, 2, true).blocks, b = norm_shape(N, H, dt, 3, true).blocks;
+  const int G = a > b ? a : b;
   return G > 1 ? (size_t)G * H * sizeof(float) : 0;
 }
 
-template <typename T, int VPT>
-void launch_fwd(const void* x, const void* r, const void* w, int N, int H, float eps, void* h, void* y,
-                int blocks, int threads, cudaStream_t s) {
-  if (r)
-    MOE_TRACED("add_rms_norm", s, (add_rms_norm_kernel<T, VPT, true><<<blocks, threads, 0, s>>>(
-                                      (const T*)x, (const T*)r, (const T*)w, N, H, eps, (T*)h, (T*)y)));
-  else
-    MOE_TRACED("rms_norm", s, (add_rms_norm_kernel<T, VPT, false><<<blocks, threads, 0, s>>>(
-                                  (const T*)x, nullptr, (const T*)w, N, H, eps, nullptr, (T*)y)));
+// Once a kernel and device: more shared memory than 48 KB.
+template <class Kernel>
+bool allow_smem(Kernel k, bool (&set)[64]) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && set[dev]) return true;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmBytes) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  if (dev >= 0 && dev < 64) set[dev] = true;
+  return true;
 }
 
-template <typename T, int VPT>
-void launch_bwd(const void* dy, const void* h, const void* w, const void* dh, int N, int H, float eps, void* dx,
-                float* part, void* dw, int blocks, int threads, cudaStream_t s) {
-  if (dh)
-    MOE_TRACED("add_rms_norm_bwd", s, (add_rms_norm_bwd_kernel<T, VPT, true><<<blocks, threads, 0, s>>>(
-                                          (const T*)dy, (const T*)h, (const T*)w, (const T*)dh, N, H, eps, (T*)dx,
-                                          part, (T*)dw)));
-  else
-    MOE_TRACED("rms_norm_bwd", s, (add_rms_norm_bwd_kernel<T, VPT, false><<<blocks, threads, 0, s>>>(
-                                      (const T*)dy, (const T*)h, (const T*)w, nullptr, N, H, eps, (T*)dx, part,
-                                      (T*)dw)));
+template <typename T, int VPT, int D, bool RES>
+bool launch_fwd(const void* x, const void* r, const void* w, int N, int H, float eps, void* h, void* y,
+                const NormShape& sh, cudaStream_t s) {
+  static bool set[64] = {false};
+  if (!allow_smem(add_rms_norm_kernel<T, VPT, D, RES>, set)) return false;
+  MOE_TRACED(RES ? "add_rms_norm" : "rms_norm", s,
+             (add_rms_norm_kernel<T, VPT, D, RES><<<sh.blocks, sh.threads, sh.smem, s>>>(
+                 (const T*)x, (const T*)r, (const T*)w, N, H, eps, (T*)h, (T*)y)));
+  return true;
+}
+template <typename T, int VPT, int D, bool DH>
+bool launch_bwd(const void* dy, const void* h, const void* w, const void* dh, int N, int H, float eps, void* dx,
+                float* part, void* dw, const NormShape& sh, cudaStream_t s) {
+  static bool set[64] = {false};
+  if (!allow_smem(add_rms_norm_bwd_kernel<T, VPT, D, DH>, set)) return false;
+  MOE_TRACED(DH ? "add_rms_norm_bwd" : "rms_norm_bwd", s,
+             (add_rms_norm_bwd_kernel<T, VPT, D, DH><<<sh.blocks, sh.threads, sh.smem, s>>>(
+                 (const T*)dy, (const T*)h, (const T*)w, (const T*)dh, N, H, eps, (T*)dx, part, (T*)dw)));
+  return true;
 }
 
-template <typename T>
+template <typename T, bool RES>
 moe_status norm_fwd(const void* x, const void* r, const void* w, int N, int H, moe_dtype dt, float eps, void* h,
                     void* y, cudaStream_t s) {
-  const NormShape sh = shape_of(H, dt, kFwdCap);
-  const int blocks = norm_blocks(N, sh.threads, kFwdThreads);
-  if (sh.vpt == 1) launch_fwd<T, 1>(x, r, w, N, H, eps, h, y, blocks, sh.threads, s);
-  else if (sh.vpt == 2) launch_fwd<T, 2>(x, r, w, N, H, eps, h, y, blocks, sh.threads, s);
-  else launch_fwd<T, 4>(x, r, w, N, H, eps, h, y, blocks, sh.threads, s);
+  const NormShape sh = norm_shape(N, H, dt, RES ? 2 : 1, false);
+  const bool deep = sh.depth == 3;
+#define MOE_NORM_FWD(VPT) (deep ? launch_fwd<T, VPT, 3, RES>(x, r, w, N, H, eps, h, y, sh, s) \
+                                : launch_fwd<T, VPT, 2, RES>(x, r, w, N, H, eps, h, y, sh, s))
+  const bool ok = sh.vpt == 1 ? MOE_NORM_FWD(1) : sh.vpt == 2 ? MOE_NORM_FWD(2) : MOE_NORM_FWD(4);
+#undef MOE_NORM_FWD
+  if (!ok) return MOE_ERR_CUDA;
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
 
-template <typename T>
+template <typename T, bool DH>
 moe_status norm_bwd(const void* dy, const void* h, const void* w, const void* dh, int N, int H, moe_dtype dt,
                     float eps, void* dx, void* dw, float* part, cudaStream_t s) {
-  const NormShape sh = shape_of(H, dt, kBwdCap);
-  const int blocks = norm_blocks(N, sh.threads, kBwdThreads);
-  if (sh.vpt == 1) launch_bwd<T, 1>(dy, h, w, dh, N, H, eps, dx, part, dw, blocks, sh.threads, s);
-  else if (sh.vpt == 2) launch_bwd<T, 2>(dy, h, w, dh, N, H, eps, dx, part, dw, blocks, sh.threads, s);
-  else launch_bwd<T, 4>(dy, h, w, dh, N, H, eps, dx, part, dw, blocks, sh.threads, s);
+  const NormShape sh = norm_shape(N, H, dt, DH ? 3 : 2, true);
+  const bool deep = sh.depth == 3;
+#define MOE_NORM_BWD(VPT) (deep ? launch_bwd<T, VPT, 3, DH>(dy, h, w, dh, N, H, eps, dx, part, dw, sh, s) \
+                                : launch_bwd<T, VPT, 2, DH>(dy, h, w, dh, N, H, eps, dx, part, dw, sh, s))
+  const bool ok = sh.vpt == 1 ? MOE_NORM_BWD(1) : sh.vpt == 2 ? MOE_NORM_BWD(2) : MOE_NORM_BWD(4);
+#undef MOE_NORM_BWD
+  if (!ok) return MOE_ERR_CUDA;
   MOE_LAUNCH_CHECK();
-  if (blocks > 1) {
-    MOE_TRACED("rms_norm_dw", s, (rms_norm_dw_kernel<T><<<(unsigned)cdiv(H, kDwCols), kDwCols * kDwRows, 0, s>>>(
-                                     part, blocks, H, (T*)dw)));
-    MOE_LAUNCH_CHECK();
+  if (sh.blocks > 1) {
+    cudaError_t err = cudaSuccess;
+    MOE_TRACED("rms_norm_dw", s,
+               (err = launch_after(rms_norm_dw_kernel<T>, (unsigned)cdiv(H, kDwCols), kDwCols * kDwRows, 0, s,
+                                   (const float*)part, sh.blocks, H, (T*)dw)));
+    if (err != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
   }
   return MOE_OK;
 }
@@ -361,8 +419,11 @@ moe_status moe_add_rms_norm(const void* x, const void* residual, const void* wei
       cross(h, all, x, all) || cross(h, all, residual, all) || cross(y, all, x, all) || cross(y, all, residual, all))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
-  return dt == MOE_F32 ? norm_fwd<float>(x, residual, weight, N, H, dt, eps, h, y, s)
-                       : norm_fwd<__nv_bfloat16>(x, residual, weight, N, H, dt, eps, h, y, s);
+  if (dt == MOE_F32)
+    return residual ? norm_fwd<float, true>(x, residual, weight, N, H, dt, eps, h, y, s)
+                    : norm_fwd<float, false>(x, nullptr, weight, N, H, dt, eps, nullptr, y, s);
+  return residual ? norm_fwd<__nv_bfloat16, true>(x, residual, weight, N, H, dt, eps, h, y, s)
+                  : norm_fwd<__nv_bfloat16, false>(x, nullptr, weight, N, H, dt, eps, nullptr, y, s);
 }
 
 size_t moe_add_rms_norm_bwd_workspace_size(int32_t N, int32_t H, moe_dtype dt) {
@@ -395,8 +456,11 @@ moe_status moe_add_rms_norm_bwd(const void* dy, const void* h, const void* weigh
     return MOE_OK;
   }
   float* part = (float*)((char*)ws + kStatusBytes);
-  return dt == MOE_F32 ? norm_bwd<float>(dy, h, weight, dh, N, H, dt, eps, dx, dweight, part, s)
-                       : norm_bwd<__nv_bfloat16>(dy, h, weight, dh, N, H, dt, eps, dx, dweight, part, s);
+  if (dt == MOE_F32)
+    return dh ? norm_bwd<float, true>(dy, h, weight, dh, N, H, dt, eps, dx, dweight, part, s)
+              : norm_bwd<float, false>(dy, h, weight, dh, N, H, dt, eps, dx, dweight, part, s);
+  return dh ? norm_bwd<__nv_bfloat16, true>(dy, h, weight, dh, N, H, dt, eps, dx, dweight, part, s)
+            : norm_bwd<__nv_bfloat16, false>(dy, h, weight, dh, N, H, dt, eps, dx, dweight, part, s);
 }
 
 }  // extern "C"
