@@ -16,8 +16,7 @@
 // A tensor is cut into 16-byte vectors from its first 16-byte boundary on, in
 // chunks of kChunkVec vectors; the few elements before and after go one by one.
 //
-// Squares are summed in fp32 over a thread's vectors of one chunk, then in double
-// over chunks.  An fp32 sum that overflowed, or so small that squares may have underflowed,
+// Squares are summed in fp32 over kSumVec vectors, then in double.  An fp32 sum that overflowed, or so small that squares may have underflowed,
 // is taken again in double, so the norm holds for gradients of any magnitude.
 #include <algorithm>
 #include <new>
@@ -32,9 +31,10 @@ namespace moe {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kChunkPer = 4;                              // vectors a thread takes of a chunk
-constexpr int kChunkVec = kClipThreads * kChunkPer;       // 16 KB
-constexpr int kClipBlocks = 148 * 8;                      // most blocks a launch (fixed: the sum's order)
+constexpr int kChunkPer = 8;                              // vectors a thread takes of a chunk
+constexpr int kChunkVec = kClipThreads * kChunkPer;       // 32 KB
+constexpr int kSumVec = 4;                                // of them added in fp32 at a time
+constexpr int kClipBlocks = 148 * 12;                     // most blocks a launch (fixed: the sum's order)
 
 struct ClipTensor {
   const void* g;
@@ -77,30 +77,34 @@ __device__ __forceinline__ double chunk_squares(const T* g, int64_t numel, int c
   const T* body = g + head;
   const int64_t v0 = (int64_t)chunk * kChunkVec;
   uint4 v[kChunkPer];
-  float s = 0.f;
-  uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < kChunkPer; ++i) {
     const int64_t at = v0 + threadIdx.x + i * kClipThreads;
     v[i] = at < nvec ? ld_nc_v4(body + at * V) : make_uint4(0, 0, 0, 0);
   }
+  double sum = 0.0;
 #pragma unroll
-  for (int i = 0; i < kChunkPer; ++i) {
-    float f[V];
-    Vec<T>::to_float(v[i], f);
-    bits |= v[i].x | v[i].y | v[i].z | v[i].w;
+  for (int h = 0; h < kChunkPer; h += kSumVec) {
+    float s = 0.f;
+    uint32_t bits = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) s = fmaf(f[j], f[j], s);
-  }
-  double sum = (double)s;
-  if (!(s > 1e-30f && s < 1e38f) && bits != 0) {
-    sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kChunkPer; ++i) {
+    for (int i = h; i < h + kSumVec; ++i) {
       float f[V];
       Vec<T>::to_float(v[i], f);
+      bits |= v[i].x | v[i].y | v[i].z | v[i].w;
 #pragma unroll
-      for (int j = 0; j < V; ++j) sum += (double)f[j] * (double)f[j];
+      for (int j = 0; j < V; ++j) s = fmaf(f[j], f[j], s);
+    }
+    if ((s > 1e-30f && s < 1e38f) || bits == 0) {
+      sum += (double)s;
+    } else {
+#pragma unroll
+      for (int i = h; i < h + kSumVec; ++i) {
+        float f[V];
+        Vec<T>::to_float(v[i], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += (double)f[j] * (double)f[j];
+      }
     }
   }
   // the elements before the first and after the last whole vector
@@ -192,7 +196,13 @@ grad_scale_kernel(const __grid_constant__ ClipTable<M> tab, const double* __rest
   __shared__ double red[kClipThreads / 32];
   double sum = 0.0;
   pdl_wait();
-  for (int i = threadIdx.x; i < n_part; i += kClipThreads) sum += part[i];
+  for (int i = threadIdx.x; i < n_part; i += 8 * kClipThreads) {     // eight loads in flight
+    double v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j * kClipThreads < n_part ? part[i + j * kClipThreads] : 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += v[j];
+  }
   const double norm = sqrt(block_sum_f64(sum, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   const double r = (double)max_norm / (norm + 1e-6);

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kNormSms = 148;      // blocks are a multiple of this (fixed: dw must not depend on the GPU)
 constexpr int kNormMaxVec = 512 * 4;   // 16-byte vectors of a row: 512 threads, 4 each
-constexpr int kDwCols = 32, kDwRows = 16;   // block of the dw reduction
+constexpr int kDwCols = 8, kDwRows = 64;    // block of the dw reduction: 32-byte columns, many rows in flight
 
 __device__ __forceinline__ void copy16(uint4* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
@@ -248,26 +248,34 @@ add_rms_norm_bwd_kernel(const T* dy, const T* h, const T* __restrict__ weight, c
   }
 }
 
-// dw[c] = sum over the blocks' partial rows: kDwRows strided sums, then those
-// in order.
+// dw[c] = sum over the blocks' partial rows: kDwRows strided sums, eight loads of
+// each in flight, then those in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(kDwCols * kDwRows)
 rms_norm_dw_kernel(const float* __restrict__ part, int G, int H, T* __restrict__ dw) {
-  __shared__ float red[kDwRows][kDwCols];
+  static_assert(kDwCols == 8 && kDwRows % 4 == 0, "four rows of eight columns a warp");
+  __shared__ float red[kDwRows / 4][kDwCols];
   const int tc = threadIdx.x % kDwCols, tr = threadIdx.x / kDwCols;
   const int c = blockIdx.x * kDwCols + tc;
   float s = 0.f;
   pdl_wait();
   if (c < H) {
-#pragma unroll 8
-    for (int g = tr; g < G; g += kDwRows) s += part[(size_t)g * H + c];
+    for (int g = tr; g < G; g += 8 * kDwRows) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = g + i * kDwRows < G ? part[(size_t)(g + i * kDwRows) * H + c] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
   }
-  red[tr][tc] = s;
+  s += __shfl_xor_sync(0xffffffffu, s, 8);
+  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  if ((threadIdx.x & 31) < kDwCols) red[tr / 4][tc] = s;
   __syncthreads();
   if (tr == 0 && c < H) {
     float t = 0.f;
 #pragma unroll
-    for (int r = 0; r < kDwRows; ++r) t += red[r][tc];
+    for (int r = 0; r < kDwRows / 4; ++r) t += red[r][tc];
     dw[c] = from_f<T>(t);
   }
 }

@@ -354,16 +354,26 @@ def moe_clip_grad_norm(grads, max_norm: float, outs=None, ws=None, norm=None) ->
             raise ValueError(f"outs: expected {n} tensors, got {len(outs)}")
     named = grads[0] if n else (ws if ws is not None else norm)
     dev = named.get_device() if named is not None else torch.cuda.current_device()
-    dts = [_dt(g) for g in grads]
-    if outs is not None and n and not grads[0].is_cuda:
-        for i, (o, g) in enumerate(zip(outs, grads)):
-            _check(f"outs[{i}]", o, g.shape, g.dtype)
     if norm is not None:
         _check("norm", norm, (1,), torch.float32)
-    ptrs = [_arg("grads", g, g.shape, g.dtype, dev) for g in grads]
-    outp = None
-    if outs is not None:
-        outp = [_arg(f"outs[{i}]", o, g.shape, g.dtype, dev) for i, (o, g) in enumerate(zip(outs, grads))]
+    dtypes = [g.dtype for g in grads]
+    lists = (grads,) if outs is None else (grads, outs)
+    # every tensor at once; what fails is named by the checks one by one
+    if not (set(dtypes) <= _DT.keys() and (outs is None or (
+            [o.dtype for o in outs] == dtypes and [o.shape for o in outs] == [g.shape for g in grads])) and
+            all({t.get_device() for t in ts} <= {dev} and all([t.is_contiguous() for t in ts]) for ts in lists) and
+            (n == 0 or grads[0].is_cuda)):
+        for i, g in enumerate(grads):
+            _dt(g)
+            if outs is not None:
+                _check(f"outs[{i}]", outs[i], g.shape, g.dtype)
+        for i, g in enumerate(grads):
+            _arg(f"grads[{i}]", g, g.shape, g.dtype, dev)
+            if outs is not None:
+                _arg(f"outs[{i}]", outs[i], g.shape, g.dtype, dev)
+    ptrs = [g.data_ptr() for g in grads]
+    outp = None if outs is None else [o.data_ptr() for o in outs]
+    dts = [_DT[d] for d in dtypes]
     if ws is None:
         ws = torch.empty(load().moe_clip_grad_norm_workspace_size(n), dtype=torch.uint8, device=f"cuda:{dev}")
     if norm is None:

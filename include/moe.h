@@ -405,7 +405,7 @@ moe_status moe_add_rms_norm_bwd(const void* dy, const void* h, const void* weigh
  * list has norm 0.
  * max_norm >= 0; infinity only takes the norm.  A norm of infinity gives
  * f = 0, a NaN norm makes every gradient NaN, as the formula has it: test *norm.
- * Sums run in fp32 within 16 KB chunks and in double beyond, in a fixed order;
+ * Sums run in fp32 over four 16-byte vectors and in double beyond, in a fixed order;
  * the norm is right whenever it is a float, also where squares are not.
  * Two launches for up to 768 tensors.  Capturable.
  * ws: moe_clip_grad_norm_workspace_size(count) bytes (never less for more
