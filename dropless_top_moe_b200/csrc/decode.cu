@@ -165,55 +165,72 @@ decode_route_kernel(const Args a, int S, int wide, int pick) {
 // ---- fp32 experts ------------------------------------------------------------
 // fp32 layers keep full single precision, so their products are FMAs.  A block
 // takes a tile of 4 CT columns (gate and up of the same ones, or down), its 256 / CT
-// row groups stream the rows, 16-byte loads, up to 16 of them in flight, and TM
-// tokens share each weight; the groups' sums are added in a fixed order.  Activations and
-// expert outputs are handed over as words that are their own flags, tiles as
-// tickets in order, so the phases run into each other.  HBM bounds it up to some
-// eight tokens an expert, FMAs beyond.
+// row groups take the rows in turn, TM tokens share each weight, and the groups'
+// sums are added in a fixed order.  Every thread copies its own weights to shared
+// memory kAhead rows ahead (cp.async): they keep coming across the barriers around the
+// tokens' staging, and need no barrier themselves.  Activations and expert outputs are
+// handed over as words that are their own flags, tiles as tickets in order, so
+// the phases run into each other.  HBM bounds it up to some eight tokens an expert,
+// FMAs beyond.
 constexpr int kThreads = 256;
 constexpr int kXRows = 512;          // rows of the tokens' operand staged at a time
 constexpr int kTokens = 8;           // most tokens at a time
+constexpr int kAhead = 8;            // rows of a thread under way or in hand
 
-// Four columns of a weight row: one 16-byte load, or (rows that are not a whole
-// number of vectors long) element by element.
-template <int CT, bool WIDE>
-__device__ __forceinline__ float4 load_w(const float* row, int ct, int c0, int cols) {
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (WIDE) {
-    if (c0 + ct * 4 < cols) v = __ldg((const float4*)(row + c0 + ct * 4));
-  } else {
-    const int c = c0 + ct;
-    if (c < cols) v.x = __ldg(row + c);
-    if (c + CT < cols) v.y = __ldg(row + c + CT);
-    if (c + 2 * CT < cols) v.z = __ldg(row + c + 2 * CT);
-    if (c + 3 * CT < cols) v.w = __ldg(row + c + 3 * CT);
-  }
-  return v;
-}
 template <int CT, bool WIDE>
 __device__ __forceinline__ int tile_col(int ct, int j) {
   return WIDE ? ct * 4 + j : j * CT + ct;
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
 }
 
 struct Smem {
   Plan plan;
   Picked pick;
+  int chunk0[kMaxExperts + 1];       // token chunks of kTokens before a slot's
   int tokens[kMaxTokens];
-  alignas(16) float xs[kTokens][kXRows];
-  alignas(16) float red[8][kTokens * 2 * 64];    // a warp's sums: [token][matrix][column]
   int ticket;
-  int ok;
+  alignas(16) float xs[kXRows][kTokens];
+  // the weights under way, [row][matrix][thread]; then a tile's sums, [warp][token][matrix][column]
+  alignas(16) float4 ring[kAhead * 2 * kThreads];
 };
-static_assert(sizeof(((Smem*)0)->red) >= 2 * kRouteCols * sizeof(float), "pick_experts' scratch");
+static_assert(sizeof(((Smem*)0)->ring) >= 2 * kRouteCols * sizeof(float), "pick_experts' scratch");
+static_assert(sizeof(((Smem*)0)->ring) >= 8 * kTokens * 2 * 64 * sizeof(float), "a tile's sums");
 
 // A tile of NM matrices for TM tokens from row t0 of a slot on:
-// C_m[t][c] = sum_r in(t, r) W_m[r][c]; put(t, c, sums) takes them.  POLL: `in` gives
-// words that may still be empty.
+// C_m[t][c] = sum_r in(t)[r] W_m[r][c]; put(t, c, sums) takes them.  POLL: the words that
+// `in` points to may still be empty.
 template <int CT, bool WIDE, bool POLL, int NM, int TM, class In, class Put>
-__device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, Smem& sm, const float* const (&W)[NM], int depth, int cols, int c0, int t0,
-                                            int cnt, In in, Put put) {
-  constexpr int RG = kThreads / CT, U = TM > 4 ? 4 : 8;   // rows in flight a thread
+__device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, Smem& sm, const float* const (&W)[NM],
+                                            int depth, int cols, int c0, int t0, int cnt, In in, Put put) {
+  constexpr int RG = kThreads / CT, C = 4 * CT;
   const int tid = threadIdx.x, ct = tid % CT, rg = tid / CT, warp = tid >> 5, lane = tid & 31;
+  const int mine = (depth - rg + RG - 1) / RG;           // rows of this thread: rg, rg + RG, ...
+  auto ask = [&](int i) {
+    if (i < mine) {
+      const size_t row = (size_t)(rg + i * RG) * cols;
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        float4* dst = &sm.ring[((i % kAhead) * NM + m) * kThreads + tid];
+        if (WIDE) {
+          if (c0 + ct * 4 < cols) copy_async<16>(dst, W[m] + row + c0 + ct * 4);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c0 + j * CT + ct < cols) copy_async<4>((float*)dst + j, W[m] + row + c0 + j * CT + ct);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) ask(i);
   float acc[TM][NM][4];
 #pragma unroll
   for (int t = 0; t < TM; ++t)
@@ -221,56 +238,63 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
     for (int m = 0; m < NM; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[t][m][j] = 0.f;
+  int i = 0;
   for (int r0 = 0; r0 < depth; r0 += kXRows) {
     const int rows = depth - r0 < kXRows ? depth - r0 : kXRows;
     __syncthreads();
-    for (int i0 = tid; i0 < TM * rows; i0 += 8 * kThreads) {      // eight values in flight
-      float v[8];
+    // 8 / TM warps a token, eight loads of a thread in flight
+    constexpr int WT = 8 / TM, STEP = 32 * WT;
+    const int t = warp / WT, first = (warp % WT) * 32 + lane;
+    if (t0 + t < cnt) {
+      const float* src = in(t0 + t) + r0;
+      for (int e0 = first; e0 < rows; e0 += 8 * STEP) {
+        float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j * kThreads, t = i / rows;
-        v[j] = i < TM * rows && t0 + t < cnt ? in(t0 + t, r0 + i - t * rows) : 0.f;
-      }
+        for (int j = 0; j < 8; ++j) {
+          v[j] = 0.f;
+          if (e0 + j * STEP < rows) v[j] = POLL ? ld_word(src + e0 + j * STEP) : __ldg(src + e0 + j * STEP);
+        }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j * kThreads, t = i / rows;
-        if (i < TM * rows) {
+        for (int j = 0; j < 8; ++j) {
+          if (e0 + j * STEP >= rows) break;
           if (POLL)
-            while (__float_as_uint(v[j]) == kEmpty && patience.again(a.cnt, a.status)) v[j] = in(t0 + t, r0 + i - t * rows);
-          sm.xs[t][i - t * rows] = v[j];
+            while (__float_as_uint(v[j]) == kEmpty && patience.again(a.cnt, a.status)) v[j] = ld_word(src + e0 + j * STEP);
+          sm.xs[e0 + j * STEP][t] = v[j];
         }
       }
     }
     __syncthreads();
-    for (int rb = rg; rb < rows; rb += RG * U) {
-      float4 w[U][NM];
+    for (; i < mine && rg + i * RG < r0 + rows; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+      float4 w[NM];
 #pragma unroll
-      for (int i = 0; i < U; ++i)
+      for (int m = 0; m < NM; ++m) w[m] = sm.ring[((i % kAhead) * NM + m) * kThreads + tid];
+      ask(i + kAhead - 1);
+      const float* xr = sm.xs[rg + i * RG - r0];
+      float xv[TM];
+      if constexpr (TM % 4 == 0) {
+#pragma unroll
+        for (int t = 0; t < TM; t += 4) *(float4*)(xv + t) = *(const float4*)(xr + t);
+      } else {
+#pragma unroll
+        for (int t = 0; t < TM; ++t) xv[t] = xr[t];
+      }
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-          w[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (rb + i * RG < rows) w[i][m] = load_w<CT, WIDE>(W[m] + (size_t)(r0 + rb + i * RG) * cols, ct, c0, cols);
+          acc[t][m][0] = fmaf(xv[t], w[m].x, acc[t][m][0]);
+          acc[t][m][1] = fmaf(xv[t], w[m].y, acc[t][m][1]);
+          acc[t][m][2] = fmaf(xv[t], w[m].z, acc[t][m][2]);
+          acc[t][m][3] = fmaf(xv[t], w[m].w, acc[t][m][3]);
         }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        if (rb + i * RG < rows) {
-#pragma unroll
-          for (int t = 0; t < TM; ++t) {
-            const float xv = sm.xs[t][rb + i * RG];
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-              acc[t][m][0] = fmaf(xv, w[i][m].x, acc[t][m][0]);
-              acc[t][m][1] = fmaf(xv, w[i][m].y, acc[t][m][1]);
-              acc[t][m][2] = fmaf(xv, w[i][m].z, acc[t][m][2]);
-              acc[t][m][3] = fmaf(xv, w[i][m].w, acc[t][m][3]);
-            }
-          }
-        }
-      }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();                    // the ring is free: the sums go there
   // the row groups of a warp, then the warps, each in a fixed order
-  constexpr int C = 4 * CT;
+  float* red = (float*)sm.ring;
+  constexpr int L = TM * NM * C;      // of a warp
 #pragma unroll
   for (int t = 0; t < TM; ++t)
 #pragma unroll
@@ -280,39 +304,34 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
         float v = acc[t][m][j];
 #pragma unroll
         for (int o = CT; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane < CT) sm.red[warp][(t * NM + m) * C + tile_col<CT, WIDE>(ct, j)] = v;
+        if (lane < CT) red[warp * L + (t * NM + m) * C + tile_col<CT, WIDE>(ct, j)] = v;
       }
   __syncthreads();
-  for (int i = tid; i < TM * C; i += kThreads) {
-    const int t = i / C, c = i - t * C;
+  for (int e = tid; e < TM * C; e += kThreads) {
+    const int t = e / C, c = e - t * C;
     if (t0 + t < cnt && c0 + c < cols) {
       float v[NM];
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         v[m] = 0.f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[m] += sm.red[q][(t * NM + m) * C + c];
+        for (int q = 0; q < 8; ++q) v[m] += red[q * L + (t * NM + m) * C + c];
       }
       put(t0 + t, c0 + c, v);
     }
   }
+  __syncthreads();
 }
 template <int CT, bool WIDE, bool POLL, int NM, class In, class Put>
-__device__ __forceinline__ void tile(const Args& a, Patience& patience, Smem& sm, const float* const (&W)[NM], int depth, int cols, int c0, int cnt, In in,
-                                     Put put) {
-  for (int t0 = 0; t0 < cnt;) {
-    const int left = cnt - t0;
-    if (left == 1) {
-      tile_tokens<CT, WIDE, POLL, NM, 1>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
-      t0 += 1;
-    } else if (left <= 4) {
-      tile_tokens<CT, WIDE, POLL, NM, 4>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
-      t0 += 4;
-    } else {
-      tile_tokens<CT, WIDE, POLL, NM, 8>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
-      t0 += 8;
-    }
-  }
+__device__ __forceinline__ void tile(const Args& a, Patience& patience, Smem& sm, const float* const (&W)[NM], int depth,
+                                     int cols, int c0, int t0, int cnt, In in, Put put) {
+  const int left = cnt - t0;
+  if (left == 1)
+    tile_tokens<CT, WIDE, POLL, NM, 1>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
+  else if (left <= 4)
+    tile_tokens<CT, WIDE, POLL, NM, 4>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
+  else
+    tile_tokens<CT, WIDE, POLL, NM, 8>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
 }
 
 template <int CT, bool WIDE>
@@ -330,14 +349,36 @@ decode_experts_kernel(const Args a, const RouteCut cut) {
   clear_plan(sm.plan, kThreads);
   pdl_wait();
   if (cut.here) {
-    pick_all(a, cut, sm.plan, sm.pick, &sm.red[0][0]);
-    build_plan(sm.plan, nullptr, a.N, a.K, a.E, kThreads);
+    pick_all(a, cut, sm.plan, sm.pick, (float*)sm.ring);
+    build_plan(sm.plan, nullptr, a.N, a.K, a.E, kThreads);    // ends with a barrier: the ring is free
   } else {
     build_plan(sm.plan, a.top, a.N, a.K, a.E, kThreads);
   }
   const int slots = sm.plan.slots;
+  if (tid < 32) {                    // eight slots a lane
+    int own[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int u = tid * 8 + i;
+      own[i] = sum;
+      if (u < slots) sum += (sm.plan.off[u + 1] - sm.plan.off[u] + kTokens - 1) / kTokens;
+    }
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (tid >= o) before += v;
+    }
+    before -= sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (tid * 8 + i <= slots) sm.chunk0[tid * 8 + i] = before + own[i];
+    if (tid == 31 && slots == kMaxExperts) sm.chunk0[slots] = before + sum;
+  }
+  __syncthreads();
+  const int chunks = sm.chunk0[slots];
   const int nft = (int)cdiv(a.F, C), nht = (int)cdiv(a.H, C);
-  const int n_up = slots * nft, n_down = slots * nht;
+  const int n_up = chunks * nft, n_down = chunks * nht;
   Patience patience;
   for (;;) {
     int t = sm.ticket;
@@ -347,8 +388,16 @@ decode_experts_kernel(const Args a, const RouteCut cut) {
     if (tid == 0) next = atomicAdd(a.queue, 1);      // arrives during this tile
     const bool up = t < n_up;
     if (!up) t -= n_up;
-    const int u = up ? t / nft : t / nht;
-    const int c0 = (up ? t % nft : t % nht) * C;
+    // a slot's tiles in turn, the token chunks of a tile next to one another: they share its weights in L2
+    const int tiles = up ? nft : nht;
+    int u = 0;
+    for (int hi = slots; hi - u > 1;) {
+      const int mid = (u + hi) >> 1;
+      if (sm.chunk0[mid] * tiles <= t) u = mid; else hi = mid;
+    }
+    t -= sm.chunk0[u] * tiles;
+    const int nch = sm.chunk0[u + 1] - sm.chunk0[u];
+    const int c0 = t / nch * C, t0 = t % nch * kTokens;
     const int e = sm.plan.expert[u], base = sm.plan.off[u], cnt = sm.plan.off[u + 1] - base;
     const size_t eo = (size_t)e * a.H * a.F;
     if (up) {
@@ -356,12 +405,12 @@ decode_experts_kernel(const Args a, const RouteCut cut) {
         sm.tokens[plan_row(sm.plan, tid, e) - base] = tid;
       const float* const W[2] = {(const float*)a.W1 + eo, (const float*)a.W3 + eo};
       tile<CT, WIDE, false, 2>(
-          a, patience, sm, W, a.H, a.F, c0, cnt, [&](int r, int h) { return __ldg(x + (size_t)sm.tokens[r] * a.H + h); },
+          a, patience, sm, W, a.H, a.F, c0, t0, cnt, [&](int r) { return x + (size_t)sm.tokens[r] * a.H; },
           [&](int r, int c, const float (&v)[2]) { st_word(act + (size_t)(base + r) * a.F + c, silu_f(v[0]) * v[1]); });
     } else {
       const float* const W[1] = {(const float*)a.W2 + eo};
       tile<CT, true, true, 1>(
-          a, patience, sm, W, a.F, a.H, c0, cnt, [&](int r, int f) { return ld_word(act + (size_t)(base + r) * a.F + f); },
+          a, patience, sm, W, a.F, a.H, c0, t0, cnt, [&](int r) { return act + (size_t)(base + r) * a.F; },
           [&](int r, int c, const float (&v)[1]) { st_word(a.out + (size_t)(base + r) * a.H + c, v[0]); });
     }
     if (tid == 0) sm.ticket = next;
