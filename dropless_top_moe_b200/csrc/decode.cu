@@ -177,17 +177,17 @@ constexpr int kXRows = 512;          // rows of the tokens' operand staged at a 
 constexpr int kTokens = 8;           // most tokens at a time
 constexpr int kAhead = 8;            // rows of a thread under way or in hand
 
+constexpr int kRingVec = 320;        // 16-byte vectors of one row of every row group, one matrix
+
 template <int CT, bool WIDE>
 __device__ __forceinline__ int tile_col(int ct, int j) {
   return WIDE ? ct * 4 + j : j * CT + ct;
 }
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+// 16 bytes to shared memory, of which the first `bytes` are read and the rest are zero.
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
 }
 
 struct Smem {
@@ -197,8 +197,8 @@ struct Smem {
   int tokens[kMaxTokens];
   int ticket;
   alignas(16) float xs[kXRows][kTokens];
-  // the weights under way, [row][matrix][thread]; then a tile's sums, [warp][token][matrix][column]
-  alignas(16) float4 ring[kAhead * 2 * kThreads];
+  // the weights under way, [row][matrix][...]; then a tile's sums, [warp][token][matrix][column]
+  alignas(16) float4 ring[kAhead * 2 * kRingVec];
 };
 static_assert(sizeof(((Smem*)0)->ring) >= 2 * kRouteCols * sizeof(float), "pick_experts' scratch");
 static_assert(sizeof(((Smem*)0)->ring) >= 8 * kTokens * 2 * 64 * sizeof(float), "a tile's sums");
@@ -211,19 +211,29 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
                                             int depth, int cols, int c0, int t0, int cnt, In in, Put put) {
   constexpr int RG = kThreads / CT, C = 4 * CT;
   const int tid = threadIdx.x, ct = tid % CT, rg = tid / CT, warp = tid >> 5, lane = tid & 31;
-  const int mine = (depth - rg + RG - 1) / RG;           // rows of this thread: rg, rg + RG, ...
+  // WIDE: every thread copies, and reads, its own vector.  Else a row starts anywhere
+  // in a vector: a row group's CT lanes copy the CT + 1 aligned vectors that cover its
+  // columns (what lies past the matrix's end is not read) and read each other's, PITCH
+  // floats a row group so that a warp's reads meet no bank twice.
+  constexpr int PITCH = WIDE ? C : (CT == 4 ? 20 : C + (CT == 8 ? 8 : 16));
+  static_assert(RG * PITCH <= kRingVec * 4, "a row of the ring");
+  const int warp_rg = warp * 32 / CT;                    // the warp's first row group
+  const int cw = cols - c0;                              // columns from the tile's first on
   auto ask = [&](int i) {
-    if (i < mine) {
-      const size_t row = (size_t)(rg + i * RG) * cols;
+    const int r = rg + i * RG;
+    if (r < depth) {
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
-        float4* dst = &sm.ring[((i % kAhead) * NM + m) * kThreads + tid];
+        float* dst = (float*)&sm.ring[((i % kAhead) * NM + m) * kRingVec] + rg * PITCH;
+        const float* src = W[m] + (size_t)r * cols + c0;
         if (WIDE) {
-          if (c0 + ct * 4 < cols) copy_async<16>(dst, W[m] + row + c0 + ct * 4);
+          if (ct * 4 < cw) copy_async(dst + ct * 4, src + ct * 4);
         } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (c0 + j * CT + ct < cols) copy_async<4>((float*)dst + j, W[m] + row + c0 + j * CT + ct);
+          const int lead = (int)(((uintptr_t)src >> 2) & 3u);          // elements before the first column
+          const int need = lead + (cw < C ? cw : C);                   // from the aligned start on
+          src -= lead;
+          if (ct * 4 < need) copy_async(dst + ct * 4, src + ct * 4, need - ct * 4 < 4 ? (need - ct * 4) * 4 : 16);
+          if (ct == 0 && C < need) copy_async(dst + C, src + C, (need - C) * 4);
         }
       }
     }
@@ -264,13 +274,24 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
       }
     }
     __syncthreads();
-    for (; i < mine && rg + i * RG < r0 + rows; ++i) {
+    for (; warp_rg + i * RG < r0 + rows; ++i) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+      if (!WIDE) __syncwarp();                  // the row group's other lanes' copies; and its slot of the last turn is read
+      const int r = rg + i * RG;
       float4 w[NM];
 #pragma unroll
-      for (int m = 0; m < NM; ++m) w[m] = sm.ring[((i % kAhead) * NM + m) * kThreads + tid];
+      for (int m = 0; m < NM; ++m) {
+        const float* at = (const float*)&sm.ring[((i % kAhead) * NM + m) * kRingVec] + rg * PITCH;
+        if (WIDE) {
+          w[m] = *(const float4*)(at + ct * 4);
+        } else {
+          at += (((uintptr_t)(W[m] + (size_t)r * cols + c0) >> 2) & 3u) + ct;
+          w[m] = make_float4(at[0], at[CT], at[2 * CT], at[3 * CT]);
+        }
+      }
       ask(i + kAhead - 1);
-      const float* xr = sm.xs[rg + i * RG - r0];
+      if (r >= depth) continue;
+      const float* xr = sm.xs[r - r0];
       float xv[TM];
       if constexpr (TM % 4 == 0) {
 #pragma unroll
@@ -588,10 +609,14 @@ moe_status experts(const Args& a, const RouteCut& cut, cudaStream_t s) {
   return MOE_OK;
 }
 moe_status experts_any(const Args& a, const RouteCut& cut, cudaStream_t s) {
-  const int64_t used = (int64_t)a.N * a.K < a.E ? (int64_t)a.N * a.K : a.E;
-  const bool narrow = used * cdiv(a.F, 64) < 4 * kBlocks;    // 32 columns a tile where 64 leave blocks without work
-  if (a.F % 4 == 0) return narrow ? experts<8, true>(a, cut, s) : experts<16, true>(a, cut, s);
-  return narrow ? experts<8, false>(a, cut, s) : experts<16, false>(a, cut, s);
+  // narrower tiles (64, 32 or 16 columns) where wider ones leave blocks without work;
+  // each stages its tokens anew
+  const int64_t pairs = (int64_t)a.N * a.K, used = pairs < a.E ? pairs : a.E;
+  const int64_t chunks = used > pairs / kTokens ? used : pairs / kTokens;
+  const int ct = chunks * cdiv(a.F, 64) >= 4 * kBlocks ? 16 : (chunks * cdiv(a.F, 32) >= 2 * kBlocks ? 8 : 4);
+  if (a.F % 4 == 0)
+    return ct == 16 ? experts<16, true>(a, cut, s) : ct == 8 ? experts<8, true>(a, cut, s) : experts<4, true>(a, cut, s);
+  return ct == 16 ? experts<16, false>(a, cut, s) : ct == 8 ? experts<8, false>(a, cut, s) : experts<4, false>(a, cut, s);
 }
 
 }  // namespace
