@@ -531,11 +531,8 @@ size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, 
   const size_t zero = sizeof(Counters) + tiles * sizeof(int);
   void* cnt = take(zero);
   void* part = take(part_bytes(N, H, E));
-  // the direct variant's activations are fp32
-  const size_t act_row = (size_t)K * F * elem(dt);
-  const size_t direct_rows = (size_t)(N < kDirectTokens ? N : kDirectTokens) * K * F * sizeof(float);
   const size_t fill0 = off;
-  void* act = take(dt == MOE_BF16 && direct_rows > N * act_row ? direct_rows : N * act_row);
+  void* act = take((size_t)N * K * F * sizeof(float));       // or two bf16 numbers each
   void* out = take((size_t)N * K * H * sizeof(float));
   void* pu = dt == MOE_BF16 ? take(umma_up_bytes(N, H, E, K, F)) : nullptr;
   void* pd = dt == MOE_BF16 ? take(umma_down_bytes(N, H, E, K, F)) : nullptr;

@@ -48,7 +48,7 @@ struct Args {
   int64_t fill_vecs;
   int zero_ints;               // the router kernel zeroes this many from cnt on
   float* logit_part;           // [groups][S][TG][E]
-  void* act;                   // [N*K][F]
+  void* act;                   // fp32 [N*K][F], or bf16 [2][N*K][F] (decode_umma.cu)
   float* out;                  // [N*K][H]
 };
 

@@ -19,6 +19,11 @@
 // the experts adds them in order while it reads them.  No sum depends on the
 // order in which blocks run.
 //
+// The activations pass to the down product as two bf16 numbers, the rounded value and
+// what the rounding left (kSplitTokens tokens a slot at most; beyond, the value alone): as
+// further columns of the same MMAs they cost next to nothing, and y is as exact
+// as with fp32 activations (relative error 0.0017, its own rounding; 0.0024 without).
+//
 // With a few tokens the time is a chain of latencies, and the hand-over between the
 // phases the longest of them: written, fenced, counted, added up, written, fenced,
 // flagged, fetched - 8 us of a 1-token call's 36 (2048/64/6/1408).  Up to kDirectTokens
@@ -55,19 +60,20 @@ constexpr int kRing = 8;                    // tickets in flight in a block
 constexpr int kLongUnits = 16;
 constexpr int kUpTickets = 2, kDownTickets = 4;    // a block, on long lines
 constexpr int kSmemData = 210 * 1024;
+constexpr int kSplitTokens = 64;
 constexpr int kPartFloats = 2 * 128;        // a token's sums of one piece
 
 struct Params {
   CUtensorMap tw1, tw3, tw2;   // [E][H][F], [E][F][H]: 64 x 64 boxes
   CUtensorMap tx;              // [N][H]: one-row boxes, gathered
-  CUtensorMap tact;            // [N*K][F]: 16-row boxes
+  CUtensorMap tact;            // [2][N*K][F]: 8-row boxes
   Args a;
   float* part_up;              // [2 * tickets][2][N][128]: a ticket's first piece, its last
   float* part_down;
   int* tile_cnt;               // [slots][F / 128] pieces that have arrived, zeroed by the router
   RouteCut cut;
   int stages;
-  int b_bytes;                 // of a stage: N rounded up to 16 rows of 128 bytes
+  int b_bytes;                 // of a stage: the most rows of 128 bytes that N tokens take
 };
 
 // A phase's line of units and its cut into tickets of q units.
@@ -124,6 +130,17 @@ __device__ __forceinline__ Ticket read_ticket(int v, const Line& up, const Line&
 }
 
 __device__ __forceinline__ int round16(int v) { return (v + 15) & ~15; }
+__device__ __forceinline__ int round8(int v) { return (v + 7) & ~7; }
+// Rows of the down product's token tile: the rounded activations from row 0 on, what is left of them from
+// row round8(cnt) on.
+__device__ __forceinline__ bool splits(int cnt) { return cnt <= kSplitTokens; }
+__device__ __forceinline__ int down_rows(int cnt) { return splits(cnt) ? 2 * round8(cnt) : round16(cnt); }
+// What rounding v to bf16 leaves; nothing of a value that is not finite as bf16.
+__device__ __forceinline__ float rest_of(float v) {
+  const float r = v - __bfloat162float(__float2bfloat16_rn(v));
+  return isfinite(r) ? r : 0.f;
+}
+__device__ __forceinline__ uint32_t rest_of2(float a, float b) { return pack_bf16x2(rest_of(a), rest_of(b)); }
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 __device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -402,7 +419,8 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       for (int pos = begin; pos < end && ok;) {
         const Piece pc = piece_at(l, pos, end);
         const int u = pc.tile / l.nj;
-        const int e = sm.plan.expert[u], r0 = sm.plan.off[u], cnt = sm.plan.off[u + 1] - r0, n16 = round16(cnt);
+        const int e = sm.plan.expert[u], r0 = sm.plan.off[u], cnt = sm.plan.off[u + 1] - r0;
+        const int rows = k.up ? round16(cnt) : down_rows(cnt);
         int g0 = a.N, g1 = a.N, g2 = a.N, g3 = a.N;        // rows past the last token read as zeros
         if (DIRECT && k.up && builder != 0) {
           for (int i = 0; i < pc.len; ++i)
@@ -438,9 +456,9 @@ decode_umma_kernel(const __grid_constant__ Params p) {
               const int t0 = up.ticket_of(a0), t1 = up.ticket_of(a0 + up.kc - 1);
               const float* first = p.part_up + entry * up.entry(t0, a0) + (f & 127);
               const float* rest = p.part_up + (f & 127);
-              uint32_t v[kDirectTokens];
+              uint32_t v[kDirectTokens], lo[kDirectTokens];
 #pragma unroll
-              for (int r = 0; r < kDirectTokens; ++r) v[r] = 0u;
+              for (int r = 0; r < kDirectTokens; ++r) v[r] = lo[r] = 0u;
               if (t0 == t1) {
                 float2 w[kDirectTokens];
                 bool miss;
@@ -455,7 +473,10 @@ decode_umma_kernel(const __grid_constant__ Params p) {
                 } while (miss && patience.again(a.cnt, a.status));
 #pragma unroll
                 for (int r = 0; r < kDirectTokens; ++r)
-                  if (r < cnt) v[r] = pack_bf16x2(w[r].x, w[r].y);
+                  if (r < cnt) {
+                    v[r] = pack_bf16x2(w[r].x, w[r].y);
+                    lo[r] = rest_of2(w[r].x, w[r].y);
+                  }
               } else {
 #pragma unroll
                 for (int r = 0; r < kDirectTokens; ++r)
@@ -481,7 +502,9 @@ decode_umma_kernel(const __grid_constant__ Params p) {
                         w.x += wq[m].x; w.y += wq[m].y;
                       }
                     }
-                    v[r] = pack_bf16x2(silu_f(g.x) * w.x, silu_f(g.y) * w.y);
+                    const float ax = silu_f(g.x) * w.x, ay = silu_f(g.y) * w.y;
+                    v[r] = pack_bf16x2(ax, ay);
+                    lo[r] = rest_of2(ax, ay);
                   }
               }
               if (lane == 0) ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
@@ -490,10 +513,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
               const uint32_t dst = base + stage * stage_bytes + kABytes;
 #pragma unroll
               for (int r = 0; r < kDirectTokens; ++r)      // 128-byte swizzle: 16-byte chunk ^ row
-                if (r < cnt)
-                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + r * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4),
-                               "r"(v[r])
-                               : "memory");
+                if (r < cnt) {
+                  const uint32_t at = dst + r * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4;
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v[r]) : "memory");
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(lo[r]) : "memory");   // row 8 + r
+                }
               fence_proxy_async();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(sm.full[stage]));
@@ -503,16 +527,19 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           }
           if (lane == 0) {
             ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
-            if (ok) mbar_expect_tx(bar(sm.full[stage]), n16 * 128);
+            if (ok) mbar_expect_tx(bar(sm.full[stage]), rows * 128);
           }
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
           if (!ok) break;
           const uint32_t dst = base + stage * stage_bytes + kABytes;
           const int kcol = (pc.k0 + i) * kKB;
           if (k.up) {
-            if (4 * lane < n16) tma_gather4(dst + lane * 512, &p.tx, bar(sm.full[stage]), kcol, g0, g1, g2, g3);
+            if (4 * lane < rows) tma_gather4(dst + lane * 512, &p.tx, bar(sm.full[stage]), kcol, g0, g1, g2, g3);
           } else {
-            if (16 * lane < n16) tma_load_2d(dst + lane * 2048, &p.tact, bar(sm.full[stage]), kcol, r0 + 16 * lane);
+            // box b: rows 8 b on; the second half of a split slot's boxes are what the rounding left
+            const int half = splits(cnt) ? rows / 16 : 16;
+            const int row = lane < half ? r0 + 8 * lane : a.N * a.K + r0 + 8 * (lane - half);
+            if (8 * lane < rows) tma_load_2d(dst + lane * 1024, &p.tact, bar(sm.full[stage]), kcol, row);
           }
           ++issued;
           if (++stage == p.stages) { stage = 0; phase ^= 1u; }
@@ -549,8 +576,8 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         for (int pos = begin; pos < end && ok;) {
           const Piece pc = piece_at(l, pos, end);
           const int u = pc.tile / l.nj;
-          const int n16 = round16(sm.plan.off[u + 1] - sm.plan.off[u]);
-          const uint32_t idesc = idesc_bf16(128, n16, true, false);
+          const int cnt = sm.plan.off[u + 1] - sm.plan.off[u];
+          const uint32_t idesc = idesc_bf16(128, k.up ? round16(cnt) : down_rows(cnt), true, false);
           ok = mbar_wait_bounded(bar(sm.tempty[acc]), acc_phase ^ 1u, abort_flag, a.status, kTimeoutNs);
           if (!ok) break;
           tc_fence_after();
@@ -586,6 +613,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
     const int et = tid - 128, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     __nv_bfloat16* act = (__nv_bfloat16*)a.act;
+    const size_t act_rest = (size_t)a.N * a.K * a.F;
+    auto put_act = [&](size_t at, float v) {
+      act[at] = __float2bfloat16_rn(v);
+      act[act_rest + at] = __float2bfloat16_rn(rest_of(v));
+    };
     const size_t entry = (size_t)a.N * kPartFloats;        // floats of a partial-sum entry
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -613,11 +645,23 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         const uint32_t d = tmem + acc * 256 + lanes;
         const int a0 = pc.tile * l.kc;
         float* part = (k.up ? p.part_up : p.part_down) + entry * l.entry(k.t, a0) + et;
+        const int rest = !k.up && splits(cnt) ? round8(cnt) : 0;    // columns from a value to its rest's
         for (int c = 0; c < cnt; c += 16) {
           uint32_t v0[16], v1[16];
           tmem_ld_16(d + c, v0);
           tmem_ld_16(d + 128 + c, v1);
           tmem_ld_wait();
+          if (rest) {
+            uint32_t l0[16], l1[16];
+            tmem_ld_16(d + rest + c, l0);
+            tmem_ld_16(d + 128 + rest + c, l1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              v0[i] = __float_as_uint(__uint_as_float(v0[i]) + __uint_as_float(l0[i]));
+              v1[i] = __float_as_uint(__uint_as_float(v1[i]) + __uint_as_float(l1[i]));
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             if (c + i >= cnt) break;
@@ -638,7 +682,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
               part[(c + i) * 128] = f0;
               part[((size_t)a.N + c + i) * 128] = f1;
             } else if (k.up) {
-              act[(size_t)(r0 + c + i) * a.F + j * 128 + et] = __float2bfloat16_rn(silu_f(f0) * f1);
+              put_act((size_t)(r0 + c + i) * a.F + j * 128 + et, silu_f(f0) * f1);
             } else {
               float* o = a.out + (size_t)(r0 + c + i) * a.H + j * 256 + et;
               o[0] = f0;
@@ -688,7 +732,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                   if (c + r < cnt)
-                    act[(size_t)(r0 + c + r) * a.F + j * 128 + et] = __float2bfloat16_rn(silu_f(g[r]) * w[r]);
+                    put_act((size_t)(r0 + c + r) * a.F + j * 128 + et, silu_f(g[r]) * w[r]);
               }
             }
           }
@@ -775,12 +819,13 @@ moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, floa
   p.part_up = part_up;
   p.part_down = part_down;
   p.tile_cnt = tile_cnt;
-  p.b_bytes = (int)round_up(a.N, 16) * 128;
+  p.b_bytes = (a.N <= kSplitTokens ? 2 * (int)round_up(a.N, 8) : 2 * kSplitTokens) * 128;
+  static_assert(2 * kSplitTokens >= kMaxTokens, "the widest slot's rows");
   p.stages = kSmemData / (kABytes + p.b_bytes);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   if (!map3(&p.tw1, a.W1, a.F, a.H, a.E, 64, 3) || !map3(&p.tw3, a.W3, a.F, a.H, a.E, 64, 3) ||
       !map3(&p.tw2, a.W2, a.H, a.F, a.E, 64, 3) || !map3(&p.tx, a.x, a.H, a.N, 1, 1, 2) ||
-      !map3(&p.tact, a.act, a.F, (uint64_t)a.N * a.K, 1, 16, 2))
+      !map3(&p.tact, a.act, a.F, (uint64_t)2 * a.N * a.K, 1, 8, 2))
     return MOE_ERR_CUDA;
   const size_t smem = (size_t)p.stages * (kABytes + p.b_bytes) + 1024;
   static bool set[64] = {false};

@@ -3,7 +3,9 @@
 Tolerance of y, from the formulas.  u = 2^-24; D(n) = n + 64 roundings for a sum
 of n products (a tensor-core step over 16 of them counted as 16 additions).
   g, u' carry D(H) u (|x| |W1|), D(H) u (|x| |W3|); silu' is below 1.1, so
-  da <= (1.1 G |u'| + |silu(g)| U) D(H) u + 8 u |a| + half |a|     (half: bf16 activations)
+  da <= (1.1 G |u'| + |silu(g)| U) D(H) u + 8 u |a| + half |a|,
+half the rounding of bf16 activations: 2^-16 as two bf16 numbers (up to 64 tokens an
+expert), 2^-8 as one,
   dout <= da |W2| + D(F) u |a| |W2|,
   dy <= sum_k w_k dout_k + 2 (K + 2) u sum_k w_k |a| |W2| + routing's error on w + half |y|.
 """
@@ -30,9 +32,9 @@ def reference(c, ids, w, K):
     tol = torch.zeros_like(y)
     lr = om.router_logits(c["x_cpu"], c["W_r_cpu"])
     dw = routing_tol(H, float(np.sqrt(np.mean(lr * lr)))) / 2
-    half_act = 2.0 ** -8 if bf16 else 0.0
     for e in torch.unique(ids).tolist():
         n, k = torch.nonzero(ids == e, as_tuple=True)
+        half_act = (2.0 ** -16 if len(n) <= 64 else 2.0 ** -8) if bf16 else 0.0
         g, u = x[n] @ W1[e], x[n] @ W3[e]
         G, Ub = x[n].abs() @ W1[e].abs(), x[n].abs() @ W3[e].abs()
         s = g * torch.sigmoid(g)
