@@ -10,7 +10,10 @@
 //
 // Router kernel: blocks over slices of H and groups of tokens; each writes its
 // slice's partial logits, and the last block of a group to arrive adds the
-// slices in order and picks the experts, a warp a token.
+// slices in order and picks the experts, a warp a token; with few logits the expert
+// kernel's blocks each do that themselves.  It also clears what the expert kernel
+// hands values over in.  5 us for 33 tokens (2048 x 64), most of it latency: the loads of
+// W_r and x, a counter's round trip, the slices' sums, K rounds of arg-max.
 //
 // Expert kernels: below for fp32, decode_umma.cu for bf16.
 #include <math.h>
@@ -142,7 +145,8 @@ decode_route_kernel(const Args a, int S, int wide, int pick) {
   }
   if (s == 0 && g == 0)
     for (int i = tid; i < a.zero_ints; i += kRouteThreads) ((int*)a.cnt)[i] = 0;
-  for (int64_t i = ((int64_t)g * S + s) * kRouteThreads + tid; i < a.fill_vecs; i += (int64_t)gridDim.y * S * kRouteThreads)
+  const int64_t all_threads = (int64_t)gridDim.y * S * kRouteThreads;
+  for (int64_t i = ((int64_t)g * S + s) * kRouteThreads + tid; i < a.fill_vecs; i += all_threads)
     a.fill[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
   if (!pick) return;                  // the expert kernel goes on from here
   __threadfence();
@@ -276,7 +280,7 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
     __syncthreads();
     for (; warp_rg + i * RG < r0 + rows; ++i) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
-      if (!WIDE) __syncwarp();                  // the row group's other lanes' copies; and its slot of the last turn is read
+      if (!WIDE) __syncwarp();          // the other lanes' copies are here, and their reads of the last turn done
       const int r = rg + i * RG;
       float4 w[NM];
 #pragma unroll
@@ -477,7 +481,6 @@ decode_experts_kernel(const Args a, const RouteCut cut) {
 // ---- host ------------------------------------------------------------------
 inline bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline size_t al256(size_t b) { return (b + 255) & ~(size_t)255; }
-inline size_t elem(moe_dtype dt) { return dt == MOE_F32 ? 4 : 2; }
 
 moe_status check(int N, int H, int E, int K, int F, moe_dtype dt) {
   if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_INVALID_ARG;

@@ -14,24 +14,27 @@
 // a phase form one line (slot, tile, k) that is cut into tickets of equal length
 // whatever the tiles' borders, so the blocks stream the same number of bytes
 // however few experts are used.  A ticket's piece of a tile that is not the whole
-// tile leaves fp32 partial sums: of gate and up, the piece that arrives last adds the pieces
-// in order and applies SwiGLU; of the down product, the weighted sum over
-// the experts adds them in order while it reads them.  No sum depends on the
-// order in which blocks run.
+// tile leaves fp32 partial sums: of gate and up, the piece that arrives last adds
+// the pieces in order and applies SwiGLU; of the down product, the weighted sum
+// over the experts adds them in order while it reads them.  No sum depends on the
+// order in which blocks run.  Measured: 8 tokens 4096/64/4/2048 (26 experts, 1.3 GB of
+// weights) 198 us, 6.5 TB/s over the whole call; 64 tokens 4096/8/2/14336 444 us, 6.4 TB/s;
+// 1 token 2048/64/6/1408 (104 MB) 30 us, of which 16 are the weights.
 //
-// The activations pass to the down product as two bf16 numbers, the rounded value and
-// what the rounding left (kSplitTokens tokens a slot at most; beyond, the value alone): as
-// further columns of the same MMAs they cost next to nothing, and y is as exact
-// as with fp32 activations (relative error 0.0017, its own rounding; 0.0024 without).
+// The activations pass to the down product as two bf16 numbers, the rounded value
+// and what the rounding left (kSplitTokens tokens a slot at most; beyond, the value
+// alone): as further columns of the same MMAs they cost 1 % at most, and y is as
+// exact as with fp32 activations (relative error 0.0017, its own rounding; 0.0024
+// without).
 //
 // With a few tokens the time is a chain of latencies, and the hand-over between the
 // phases the longest of them: written, fenced, counted, added up, written, fenced,
 // flagged, fetched - 8 us of a 1-token call's 36 (2048/64/6/1408).  Up to kDirectTokens
-// tokens the partial sums carry their own flag instead: the router kernel
-// fills their buffers with a NaN that no sum has (kEmpty), readers poll the very words that they
-// need, and five warps build the down product's token tiles from them.  With more
-// tokens those tiles would be rebuilt from partial sums more often than they
-// are worth.
+// tokens the partial sums carry their own flag instead: the router kernel fills
+// their buffers with a NaN that no sum has (kEmpty), readers poll the very words
+// that they need, and five warps build the down product's token tiles from them.
+// With more tokens those tiles would be rebuilt from partial sums more often than
+// they are worth.
 //
 // One block an SM, tickets taken in order (decode.cuh says why that cannot
 // deadlock).  Warp 0 takes tickets and streams weights, running up to the whole
@@ -131,8 +134,8 @@ __device__ __forceinline__ Ticket read_ticket(int v, const Line& up, const Line&
 
 __device__ __forceinline__ int round16(int v) { return (v + 15) & ~15; }
 __device__ __forceinline__ int round8(int v) { return (v + 7) & ~7; }
-// Rows of the down product's token tile: the rounded activations from row 0 on, what is left of them from
-// row round8(cnt) on.
+// Rows of the down product's token tile: the rounded activations from row 0 on, what
+// the rounding left of them from row round8(cnt) on.
 __device__ __forceinline__ bool splits(int cnt) { return cnt <= kSplitTokens; }
 __device__ __forceinline__ int down_rows(int cnt) { return splits(cnt) ? 2 * round8(cnt) : round16(cnt); }
 // What rounding v to bf16 leaves; nothing of a value that is not finite as bf16.
@@ -320,8 +323,9 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const int slots = sm.plan.slots;
-  // tokens a slot / 4: 60 tokens on each of two experts 2432/640, 77 us without, 54 with; and
-  // eight units, which save short tiles from being cut (61 tokens 256/6/4/1024: 38 us, 30)
+  // a quarter of the mean tokens a slot (60 tokens on each of two experts 2432/640: 77 us
+  // without, 54 with), and eight units, so that short tiles stay whole (61 tokens
+  // 256/6/4/1024: 38 us without, 30 with); four in the direct variant, where cuts cost less
   const int mean4 = (a.N * a.K / slots + 3) / 4, few = DIRECT ? 4 : 8, least = mean4 > few ? mean4 : few;
   const Line up = make_line(slots, a.F / 128, a.H / kKB, kUpTickets, least);
   const Line down = make_line(slots, (a.H + 255) / 256, a.F / kKB, kDownTickets, least);

@@ -2,7 +2,7 @@
 // and backward (rows of H, one learned weight per column):
 //   forward    h = round(x + r)   (r may be absent: h = x),
 //              s = 1 / sqrt(mean_j h_j^2 + eps),  y = h * s * w
-//   backward   g = dy * w,  dx = s * g - h * s^3 * mean_j(g_j h_j) + dh,
+//   backward   g = dy * w,  dx = s * g - h * s^3 * mean_j(g_j h_j) + dh  (dh may be absent),
 //              dw_j = sum_n dy_nj * h_nj * s_n
 // h is the residual stream as it is kept, rounded to the element type, and y
 // is the norm of that rounded h: the backward pass reads h, so it

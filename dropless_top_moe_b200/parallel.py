@@ -24,6 +24,7 @@ import torch
 import torch.distributed as dist
 
 from ._lib import MOE_BF16, MOE_F32, call
+from .ops import moe_clip_grad_norm
 
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -39,10 +40,20 @@ def ordered_sum(recv: torch.Tensor, world: int, scale: float, out: torch.Tensor)
 
 def allreduce_grads(tensors: Iterable[torch.Tensor], group: Optional[dist.ProcessGroup] = None,
                     average: bool = True, chunk_elems: int = 1 << 26,
-                    local_sum: Callable[[torch.Tensor, int, float, torch.Tensor], None] = ordered_sum) -> None:
+                    local_sum: Callable[[torch.Tensor, int, float, torch.Tensor], None] = ordered_sum,
+                    max_norm: Optional[float] = None) -> Optional[torch.Tensor]:
     """Sum (or average) each tensor over the ranks of `group`, in place,
     deterministically.  Tensors must be contiguous float32 or bfloat16.
-    local_sum(recv [world, shard], world, scale, out) is step 2."""
+    local_sum(recv [world, shard], world, scale, out) is step 2.
+    max_norm: then also scale them to a global norm of at most that much
+    (moe_clip_grad_norm; every rank holds the same gradients by then, so it scales by
+    the same bits), and return the norm they had."""
+    tensors = list(tensors)
+    _reduce(tensors, group, average, chunk_elems, local_sum)
+    return None if max_norm is None else moe_clip_grad_norm(tensors, max_norm)
+
+
+def _reduce(tensors, group, average: bool, chunk_elems: int, local_sum) -> None:
     world = dist.get_world_size(group)
     if world == 1:
         return

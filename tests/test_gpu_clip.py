@@ -153,3 +153,19 @@ def test_replays_from_a_graph_with_new_gradients():
         graph.replay()
         torch.cuda.synchronize()
         check(norm, outs, grads, 1.0)
+
+
+def test_the_data_parallel_reduction_clips(tmp_path):
+    """allreduce_grads with a limit, on one rank: the reduction has nothing to add, the clipping runs."""
+    import torch.distributed as dist
+    from dropless_top_moe_b200.parallel import allreduce_grads
+
+    dist.init_process_group("gloo", store=dist.FileStore(str(tmp_path / "store"), 1), rank=0, world_size=1)
+    try:
+        grads = [rand((100, 30), torch.bfloat16, 1), rand((77,), torch.float32, 2)]
+        keep = [g.clone() for g in grads]
+        assert allreduce_grads(grads) is None
+        assert all(torch.equal(g, k) for g, k in zip(grads, keep))
+        check(allreduce_grads(grads, max_norm=1.5), grads, keep, 1.5)
+    finally:
+        dist.destroy_process_group()
