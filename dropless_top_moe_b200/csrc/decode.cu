@@ -82,6 +82,15 @@ decode_route_kernel(const Args a, int S, int wide, int pick) {
   pdl_launch();
   const int tid = threadIdx.x, g = blockIdx.y, s = blockIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
+  auto fill = [&]() {
+    const int64_t all = (int64_t)gridDim.y * gridDim.x * kRouteThreads;
+    for (int64_t i = ((int64_t)g * gridDim.x + s) * kRouteThreads + tid; i < a.fill_vecs; i += all)
+      a.fill[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+  };
+  if (s >= S) {                 // a block past the slices: there to fill
+    fill();
+    return;
+  }
   const T* x = (const T*)a.x;
   const T* wr = (const T*)a.W_r;
   const int E = a.E, H = a.H;
@@ -145,9 +154,7 @@ decode_route_kernel(const Args a, int S, int wide, int pick) {
   }
   if (s == 0 && g == 0)
     for (int i = tid; i < a.zero_ints; i += kRouteThreads) ((int*)a.cnt)[i] = 0;
-  const int64_t all_threads = (int64_t)gridDim.y * S * kRouteThreads;
-  for (int64_t i = ((int64_t)g * S + s) * kRouteThreads + tid; i < a.fill_vecs; i += all_threads)
-    a.fill[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+  fill();
   if (!pick) return;                  // the expert kernel goes on from here
   __threadfence();
   __syncthreads();
@@ -561,7 +568,9 @@ size_t carve(Args* a, UmmaWs* w, char* base, int N, int H, int E, int K, int F, 
 
 template <typename T, int TG>
 void route(const Args& a, const RouteCut& c, int pick, cudaStream_t s) {
-  const dim3 grid(c.S, c.groups);
+  // blocks for the filling, where the slices leave SMs free
+  const int fillers = a.fill_vecs > 0 && c.S * c.groups < kBlocks ? kBlocks / c.groups - c.S : 0;
+  const dim3 grid(c.S + fillers, c.groups);
   const int wide = a.E % (c.EP / 32) == 0;
 #define MOE_DECODE_ROUTE(V)                                                                                    \
   case 32 * V:                                                                                                 \

@@ -704,13 +704,15 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           if (!whole) {
             // the last piece of the tile to arrive adds them all
             const int t0 = l.ticket_of(a0), t1 = l.ticket_of(a0 + l.kc - 1);
-            __threadfence();
             epi_barrier();
-            if (et == 0) sm.last = atomicAdd(p.tile_cnt + pc.tile, 1) == t1 - t0;
+            if (et == 0) {
+              __threadfence();      // one thread's fence covers what the barrier has ordered before it
+              sm.last = atomicAdd(p.tile_cnt + pc.tile, 1) == t1 - t0;
+              __threadfence();
+            }
             epi_barrier();
             finish = sm.last != 0;
             if (finish) {
-              __threadfence();
               // gate at q, up N * 128 floats on; four pieces of four tokens in flight
               const float* first = p.part_up + entry * l.entry(t0, a0) + et;
               const float* rest = p.part_up + et;
@@ -742,7 +744,6 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           }
           if (finish) {
             fence_proxy_async_global();
-            __threadfence();
             epi_barrier();
             if (et == 0) add_release(a.cnt->done_act + u, 1);
           }
@@ -751,7 +752,6 @@ decode_umma_kernel(const __grid_constant__ Params p) {
       }
       if (!ok) break;
       if (!DIRECT && !k.up) {
-        __threadfence();
         epi_barrier();
         if (et == 0) add_release(&a.cnt->done_down, 1);
       }
