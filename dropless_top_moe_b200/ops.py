@@ -8,6 +8,7 @@ in Python.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import Optional
 
 import torch
@@ -378,13 +379,12 @@ def moe_clip_grad_norm(grads, max_norm: float, outs=None, ws=None, norm=None) ->
         ws = torch.empty(load().moe_clip_grad_norm_workspace_size(n), dtype=torch.uint8, device=f"cuda:{dev}")
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=f"cuda:{dev}")
-    if n:
-        P = ctypes.c_void_p * n
-        lists = (P(*ptrs), None if outp is None else P(*outp), (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
-                 (ctypes.c_int32 * n)(*dts))
-    else:
-        lists = (None, None, None, None)
-    _call_on(dev, "moe_clip_grad_norm", *lists, n, max_norm, _arg("norm", norm, (1,), torch.float32, dev),
+    # the host arrays that the call reads, pointers and sizes in one
+    host = array("q", ptrs + (outp or []) + [g.numel() for g in grads])
+    types = array("i", dts)
+    at, word = host.buffer_info()[0], 8 * n
+    _call_on(dev, "moe_clip_grad_norm", at, None if outp is None else at + word, at + (word if outp is None else 2 * word),
+             types.buffer_info()[0], n, max_norm, _arg("norm", norm, (1,), torch.float32, dev),
              _arg("ws", ws, (ws.numel(),), torch.uint8, dev), ws.numel())
     return norm
 
