@@ -713,32 +713,46 @@ decode_umma_kernel(const __grid_constant__ Params p) {
             epi_barrier();
             finish = sm.last != 0;
             if (finish) {
-              // gate at q, up N * 128 floats on; four pieces of four tokens in flight
-              const float* first = p.part_up + entry * l.entry(t0, a0) + et;
-              const float* rest = p.part_up + et;
-              for (int c = 0; c < cnt; c += 4) {
-                float g[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int t = t0; t <= t1; t += 4) {
-                  float gq[4][4], wq[4][4];
+              // a warp a token, four columns a lane; gate at q, up N * 128 floats on; three
+              // pieces of four tokens in flight
+              constexpr int PT = 3, TT = 4;
+              const float* first = p.part_up + entry * l.entry(t0, a0) + lane * 4;
+              const float* more = p.part_up + lane * 4;
+              for (int c = quarter; c < cnt; c += 4 * TT) {
+                float4 g[TT], w[TT];
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const float* q = (t + i == t0 ? first : rest + entry * (2 * (t + i))) + (size_t)c * 128;
+                for (int r = 0; r < TT; ++r) g[r] = w[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int t = t0; t <= t1; t += PT) {
+                  float4 gq[PT][TT], wq[PT][TT];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                      const bool in = t + i <= t1 && c + r < cnt;
-                      gq[i][r] = in ? __ldcg(q + r * 128) : 0.f;
-                      wq[i][r] = in ? __ldcg(q + ((size_t)a.N + r) * 128) : 0.f;
+                  for (int i = 0; i < PT; ++i) {
+                    const float* q = (t + i == t0 ? first : more + entry * (2 * (t + i))) + (size_t)c * 128;
+#pragma unroll
+                    for (int r = 0; r < TT; ++r) {
+                      gq[i][r] = wq[i][r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                      if (t + i <= t1 && c + 4 * r < cnt) {
+                        gq[i][r] = __ldcg((const float4*)(q + r * 512));
+                        wq[i][r] = __ldcg((const float4*)(q + (size_t)a.N * 128 + r * 512));
+                      }
                     }
                   }
 #pragma unroll
-                  for (int i = 0; i < 4; ++i)
+                  for (int i = 0; i < PT; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) { g[r] += gq[i][r]; w[r] += wq[i][r]; }
+                    for (int r = 0; r < TT; ++r) {
+                      g[r].x += gq[i][r].x; g[r].y += gq[i][r].y; g[r].z += gq[i][r].z; g[r].w += gq[i][r].w;
+                      w[r].x += wq[i][r].x; w[r].y += wq[i][r].y; w[r].z += wq[i][r].z; w[r].w += wq[i][r].w;
+                    }
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (c + r < cnt)
-                    put_act((size_t)(r0 + c + r) * a.F + j * 128 + et, silu_f(g[r]) * w[r]);
+                for (int r = 0; r < TT; ++r)
+                  if (c + 4 * r < cnt) {
+                    const float v0 = silu_f(g[r].x) * w[r].x, v1 = silu_f(g[r].y) * w[r].y;
+                    const float v2 = silu_f(g[r].z) * w[r].z, v3 = silu_f(g[r].w) * w[r].w;
+                    const size_t at = (size_t)(r0 + c + 4 * r) * a.F + j * 128 + lane * 4;
+                    *(uint2*)(act + at) = make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
+                    *(uint2*)(act + act_rest + at) = make_uint2(rest_of2(v0, v1), rest_of2(v2, v3));
+                  }
               }
             }
           }
