@@ -248,20 +248,17 @@ def moe_aux_loss(probs, bins, K: int, alpha: float, ws=None):
     return loss, P
 
 
-def _arg(name: str, t: torch.Tensor, shape, dtype, dev: Optional[int]):
+def _arg(name: str, t: torch.Tensor, shape, dtype, dev: int):
     """Pointer of an argument, after the checks of _check and _p; dev: index of the device it has to be on.
-    One pass, since small calls are bound by the host."""
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    One condition where all is well, since small calls are bound by the host."""
+    if dev >= 0 and t.get_device() == dev and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _check(name, t, shape, dtype)
     if not t.is_cuda:
         raise ValueError(f"{name}: tensors must live on a CUDA device")
     if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, the other tensors on cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensors must be contiguous")
-    return t.data_ptr()
+        raise ValueError(f"{name}: on {t.device}, the other tensors on {'cuda:%d' % dev if dev >= 0 else 'the CPU'}")
+    raise ValueError(f"{name}: tensors must be contiguous")
 
 
 # the current stream's handle, without a Stream object where torch offers that

@@ -155,6 +155,20 @@ def test_replays_from_a_graph_with_new_gradients():
         check(norm, outs, grads, 1.0)
 
 
+def test_a_tensor_of_more_than_32_bits_of_elements():
+    n = (1 << 32) + 4097
+    g = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    g.normal_(generator=torch.Generator(device="cuda").manual_seed(5))
+    ref = math.sqrt(sum(float(p.double().square().sum()) for p in g.split(1 << 27)))
+    keep = {k: g[k:k + 1000].clone() for k in (0, (1 << 31) - 500, (1 << 32) - 500, n - 1000)}
+    norm = moe.moe_clip_grad_norm([g], 100.0)
+    assert abs(float(norm) - ref) <= 17 * U * ref
+    for k, v in keep.items():
+        want = v.double() * (100.0 / (ref + 1e-6))
+        tol = want.abs() * (torch.finfo(g.dtype).eps / 2 + 20 * U) + torch.finfo(g.dtype).tiny
+        assert bool(((g[k:k + 1000].double() - want).abs() <= tol).all()), k
+
+
 def test_the_data_parallel_reduction_clips(tmp_path):
     """allreduce_grads with a limit, on one rank: the reduction has nothing to add, the clipping runs."""
     import torch.distributed as dist

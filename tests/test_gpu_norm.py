@@ -154,6 +154,23 @@ def test_in_place(dtype):
         assert torch.equal(dx, dx0) and torch.equal(dw, dw0)
 
 
+def test_more_than_32_bits_of_elements():
+    N, H = (1 << 32) // 8192 + 77, 8192
+    x = torch.empty((N, H), dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(5))
+    w = rand((H,), torch.bfloat16, 2)
+    rows = [0, 1, (1 << 31) // H, (1 << 32) // H - 1, (1 << 32) // H, N - 1]
+    keep = x[rows].clone()
+    y, h = moe.moe_add_rms_norm(x, w, eps=EPS, y=x)
+    assert y is x
+    check_forward(y[rows], keep, keep, None, w)
+    dx, _ = moe.moe_add_rms_norm_bwd(y, y, w, eps=EPS, dx=None)
+    for i in rows:
+        dx64, size, _, _ = backward64(y[i:i + 1], y[i:i + 1], w, None, EPS)
+        tol = dx64.abs() * half(dx.dtype) + size * 128 * U + tiny(dx.dtype)
+        assert bool(((dx[i:i + 1].double() - dx64).abs() <= tol).all()), i
+
+
 def test_gradient_against_differences():
     """Directional derivatives of sum(y * dy) + sum(h * dh) by central differences of the
     formula in 64 bits.  With a step of 1e-4 the cubic term is below 1e-6 relative."""
