@@ -207,7 +207,7 @@ struct Smem {
   int chunk0[kMaxExperts + 1];       // token chunks of kTokens before a slot's
   int tokens[kMaxTokens];
   int ticket;
-  alignas(16) float xs[kXRows][kTokens];
+  alignas(16) float xs[kXRows * kTokens];        // [row][token]
   // the weights under way, [row][matrix][...]; then a tile's sums, [warp][token][matrix][column]
   alignas(16) float4 ring[kAhead * 2 * kRingVec];
 };
@@ -229,23 +229,38 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
   constexpr int PITCH = WIDE ? C : (CT == 4 ? 20 : C + (CT == 8 ? 8 : 16));
   static_assert(RG * PITCH <= kRingVec * 4, "a row of the ring");
   const int warp_rg = warp * 32 / CT;                    // the warp's first row group
-  const int cw = cols - c0;                              // columns from the tile's first on
+  // A thread's rows are RG apart, and RG is a multiple of 4: where its columns start in
+  // an aligned vector, and so what each of its copies takes, is the same in every row.
+  constexpr int SLOT = NM * kRingVec * 16;               // bytes of a row of every row group
+  static_assert(RG % 4 == 0, "a thread's rows start alike");
+  const float* src[NM];                                  // the thread's vector of the next row to ask for
+  int own[NM], tail[NM];                                 // bytes of it, and of the vector past the CT-th
+  int at[NM];                                            // where in a slot the thread reads
+#pragma unroll
+  for (int m = 0; m < NM; ++m) {
+    const float* p = W[m] + (size_t)rg * cols + c0;
+    const int lead = WIDE ? 0 : (int)(((uintptr_t)p >> 2) & 3u);        // elements before the first column
+    const int need = lead + (cols - c0 < C ? cols - c0 : C);            // from the aligned start on
+    const int mine = need - ct * 4, past = need - C;
+    src[m] = p - lead + ct * 4;
+    own[m] = mine < 0 ? 0 : (mine < 4 ? mine * 4 : 16);
+    tail[m] = ct == 0 && past > 0 ? past * 4 : 0;
+    at[m] = (m * kRingVec * 4 + rg * PITCH + (WIDE ? ct * 4 : lead + ct)) * (int)sizeof(float);
+  }
+  char* const mine = (char*)sm.ring + (rg * PITCH + ct * 4) * sizeof(float);     // where in a slot it copies to
+  const size_t step = (size_t)RG * cols;
   auto ask = [&](int i) {
-    const int r = rg + i * RG;
-    if (r < depth) {
+    if (rg + i * RG < depth) {
+      char* dst = mine + (i % kAhead) * SLOT;
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
-        float* dst = (float*)&sm.ring[((i % kAhead) * NM + m) * kRingVec] + rg * PITCH;
-        const float* src = W[m] + (size_t)r * cols + c0;
         if (WIDE) {
-          if (ct * 4 < cw) copy_async(dst + ct * 4, src + ct * 4);
+          if (own[m] > 0) copy_async(dst + m * kRingVec * 16, src[m]);
         } else {
-          const int lead = (int)(((uintptr_t)src >> 2) & 3u);          // elements before the first column
-          const int need = lead + (cw < C ? cw : C);                   // from the aligned start on
-          src -= lead;
-          if (ct * 4 < need) copy_async(dst + ct * 4, src + ct * 4, need - ct * 4 < 4 ? (need - ct * 4) * 4 : 16);
-          if (ct == 0 && C < need) copy_async(dst + C, src + C, (need - C) * 4);
+          if (own[m] > 0) copy_async(dst + m * kRingVec * 16, src[m], own[m]);
+          if (tail[m] > 0) copy_async(dst + m * kRingVec * 16 + CT * 16, src[m] + C, tail[m]);
         }
+        src[m] += step;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -263,24 +278,25 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
   for (int r0 = 0; r0 < depth; r0 += kXRows) {
     const int rows = depth - r0 < kXRows ? depth - r0 : kXRows;
     __syncthreads();
-    // 8 / TM warps a token, eight loads of a thread in flight
-    constexpr int WT = 8 / TM, STEP = 32 * WT;
-    const int t = warp / WT, first = (warp % WT) * 32 + lane;
+    // a warp reads eight rows (32 bytes) of four tokens, whose words meet few banks twice;
+    // eight loads of a thread in flight
+    constexpr int XT = TM < 4 ? TM : 4, STEP = kThreads / TM;
+    const int t = lane % XT + XT * (warp % (TM / XT)), first = lane / XT + 32 / XT * (warp / (TM / XT));
     if (t0 + t < cnt) {
-      const float* src = in(t0 + t) + r0;
+      const float* row = in(t0 + t) + r0;
       for (int e0 = first; e0 < rows; e0 += 8 * STEP) {
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[j] = 0.f;
-          if (e0 + j * STEP < rows) v[j] = POLL ? ld_word(src + e0 + j * STEP) : __ldg(src + e0 + j * STEP);
+          if (e0 + j * STEP < rows) v[j] = POLL ? ld_word(row + e0 + j * STEP) : __ldg(row + e0 + j * STEP);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (e0 + j * STEP >= rows) break;
           if (POLL)
-            while (__float_as_uint(v[j]) == kEmpty && patience.again(a.cnt, a.status)) v[j] = ld_word(src + e0 + j * STEP);
-          sm.xs[e0 + j * STEP][t] = v[j];
+            while (__float_as_uint(v[j]) == kEmpty && patience.again(a.cnt, a.status)) v[j] = ld_word(row + e0 + j * STEP);
+          sm.xs[(e0 + j * STEP) * TM + t] = v[j];
         }
       }
     }
@@ -289,20 +305,19 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
       asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
       if (!WIDE) __syncwarp();          // the other lanes' copies are here, and their reads of the last turn done
       const int r = rg + i * RG;
+      const char* slot = (const char*)sm.ring + (i % kAhead) * SLOT;
       float4 w[NM];
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
-        const float* at = (const float*)&sm.ring[((i % kAhead) * NM + m) * kRingVec] + rg * PITCH;
-        if (WIDE) {
-          w[m] = *(const float4*)(at + ct * 4);
-        } else {
-          at += (((uintptr_t)(W[m] + (size_t)r * cols + c0) >> 2) & 3u) + ct;
-          w[m] = make_float4(at[0], at[CT], at[2 * CT], at[3 * CT]);
-        }
+        const float* in_slot = (const float*)(slot + at[m]);
+        if (WIDE)
+          w[m] = *(const float4*)in_slot;
+        else
+          w[m] = make_float4(in_slot[0], in_slot[CT], in_slot[2 * CT], in_slot[3 * CT]);
       }
       ask(i + kAhead - 1);
       if (r >= depth) continue;
-      const float* xr = sm.xs[r - r0];
+      const float* xr = sm.xs + (r - r0) * TM;
       float xv[TM];
       if constexpr (TM % 4 == 0) {
 #pragma unroll
