@@ -175,7 +175,7 @@ decode_route_kernel(const Args a, int S, int wide, int pick) {
 
 // ---- fp32 experts ------------------------------------------------------------
 // fp32 layers keep full single precision, so their products are FMAs.  A block
-// takes a tile of 4 CT columns (gate and up of the same ones, or down), its 256 / CT
+// takes a tile of 4 CT columns (gate and up of the same ones; down has a CT of its own), its 256 / CT
 // row groups take the rows in turn, TM tokens share each weight, and the groups'
 // sums are added in a fixed order.  Every thread copies its own weights to shared
 // memory kAhead rows ahead (cp.async): they keep coming across the barriers around the
@@ -381,12 +381,12 @@ __device__ __forceinline__ void tile(const Args& a, Patience& patience, Smem& sm
     tile_tokens<CT, WIDE, POLL, NM, 8>(a, patience, sm, W, depth, cols, c0, t0, cnt, in, put);
 }
 
-template <int CT, bool WIDE>
+template <int CT, int CTD, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_experts_kernel(const Args a, const RouteCut cut) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-  constexpr int C = 4 * CT;
+  constexpr int C = 4 * CT, CD = 4 * CTD;
   const int tid = threadIdx.x;
   const float* x = (const float*)a.x;
   float* act = (float*)a.act;
@@ -424,7 +424,7 @@ decode_experts_kernel(const Args a, const RouteCut cut) {
   }
   __syncthreads();
   const int chunks = sm.chunk0[slots];
-  const int nft = (int)cdiv(a.F, C), nht = (int)cdiv(a.H, C);
+  const int nft = (int)cdiv(a.F, C), nht = (int)cdiv(a.H, CD);
   const int n_up = chunks * nft, n_down = chunks * nht;
   Patience patience;
   for (;;) {
@@ -444,7 +444,7 @@ decode_experts_kernel(const Args a, const RouteCut cut) {
     }
     t -= sm.chunk0[u] * tiles;
     const int nch = sm.chunk0[u + 1] - sm.chunk0[u];
-    const int c0 = t / nch * C, t0 = t % nch * kTokens;
+    const int c0 = t / nch * (up ? C : CD), t0 = t % nch * kTokens;
     const int e = sm.plan.expert[u], base = sm.plan.off[u], cnt = sm.plan.off[u + 1] - base;
     const size_t eo = (size_t)e * a.H * a.F;
     if (up) {
@@ -456,7 +456,7 @@ decode_experts_kernel(const Args a, const RouteCut cut) {
           [&](int r, int c, const float (&v)[2]) { st_word(act + (size_t)(base + r) * a.F + c, silu_f(v[0]) * v[1]); });
     } else {
       const float* const W[1] = {(const float*)a.W2 + eo};
-      tile<CT, true, true, 1>(
+      tile<CTD, true, true, 1>(
           a, patience, sm, W, a.F, a.H, c0, t0, cnt, [&](int r) { return act + (size_t)(base + r) * a.F; },
           [&](int r, int c, const float (&v)[1]) { st_word(a.out + (size_t)(base + r) * a.H + c, v[0]); });
     }
@@ -610,13 +610,13 @@ moe_status route_any(const Args& a, const RouteCut& c, int pick, cudaStream_t s)
   return MOE_OK;
 }
 
-template <int CT, bool WIDE>
+template <int CT, int CTD, bool WIDE>
 moe_status experts(const Args& a, const RouteCut& cut, cudaStream_t s) {
   static bool set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (cudaFuncSetAttribute(decode_experts_kernel<CT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode_experts_kernel<CT, CTD, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)sizeof(Smem)) != cudaSuccess) {
       (void)cudaGetLastError();
       return MOE_ERR_CUDA;
@@ -624,7 +624,7 @@ moe_status experts(const Args& a, const RouteCut& cut, cudaStream_t s) {
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   cudaError_t err = cudaSuccess;
-  MOE_TRACED("decode_experts", s, (err = launch_after(decode_experts_kernel<CT, WIDE>, 2 * kBlocks, kThreads, sizeof(Smem),
+  MOE_TRACED("decode_experts", s, (err = launch_after(decode_experts_kernel<CT, CTD, WIDE>, 2 * kBlocks, kThreads, sizeof(Smem),
                                                       s, a, cut)));
   if (err != cudaSuccess) {
     (void)cudaGetLastError();
@@ -632,15 +632,26 @@ moe_status experts(const Args& a, const RouteCut& cut, cudaStream_t s) {
   }
   return MOE_OK;
 }
+template <int CT, int CTD>
+moe_status experts_at(const Args& a, const RouteCut& cut, bool wide, cudaStream_t s) {
+  return wide ? experts<CT, CTD, true>(a, cut, s) : experts<CT, CTD, false>(a, cut, s);
+}
 moe_status experts_any(const Args& a, const RouteCut& cut, cudaStream_t s) {
-  // narrower tiles (64, 32 or 16 columns) where wider ones leave blocks without work;
-  // each stages its tokens anew
-  const int64_t pairs = (int64_t)a.N * a.K, used = pairs < a.E ? pairs : a.E;
-  const int64_t chunks = used > pairs / kTokens ? used : pairs / kTokens;
-  const int ct = chunks * cdiv(a.F, 64) >= 4 * kBlocks ? 16 : (chunks * cdiv(a.F, 32) >= 2 * kBlocks ? 8 : 4);
-  if (a.F % 4 == 0)
-    return ct == 16 ? experts<16, true>(a, cut, s) : ct == 8 ? experts<8, true>(a, cut, s) : experts<4, true>(a, cut, s);
-  return ct == 16 ? experts<16, false>(a, cut, s) : ct == 8 ? experts<8, false>(a, cut, s) : experts<4, false>(a, cut, s);
+  // Tiles of 64 columns where they keep the blocks busy, else narrower ones: each stages
+  // its tokens anew and has its start and end to itself.  Up has 32 and 16 columns, down,
+  // whose tiles need the least, 16.  13 tokens on 36 experts of 1884/186: down 64 wide
+  // 59 us, 32 64, 16 77; one token on two of 1024/1024: 24, 20, 18.  Gate and up of the
+  // former 64 wide 59 us, 32 57; of 32 tokens on 16 experts of 1024/1001 96 and 90.
+  const double pairs = (double)a.N * a.K;
+  const double used = a.E * (1.0 - pow(1.0 - (double)a.K / a.E, a.N));     // experts, of a routing without a bias
+  const double chunks = used > pairs / kTokens ? used : pairs / kTokens;
+  const int ct = chunks * cdiv(a.F, 64) >= 2 * kBlocks ? 16 : (chunks * cdiv(a.F, 32) >= 2 * kBlocks ? 8 : 4);
+  const bool wide = a.F % 4 == 0;
+  if (chunks * cdiv(a.H, 64) >= kBlocks)
+    return ct == 16 ? experts_at<16, 16>(a, cut, wide, s)
+                    : ct == 8 ? experts_at<8, 16>(a, cut, wide, s) : experts_at<4, 16>(a, cut, wide, s);
+  return ct == 16 ? experts_at<16, 4>(a, cut, wide, s)
+                  : ct == 8 ? experts_at<8, 4>(a, cut, wide, s) : experts_at<4, 4>(a, cut, wide, s);
 }
 
 }  // namespace
