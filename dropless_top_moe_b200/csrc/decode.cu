@@ -201,6 +201,22 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
                : "memory");
 }
 
+// two sums in one instruction: c = a * b + c, each rounded as fmaf's (1 to 4 % of a layer's time,
+// most with many tokens an expert: issue slots bound it there)
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+
 struct Smem {
   Plan plan;
   Picked pick;
@@ -267,13 +283,13 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
   };
 #pragma unroll
   for (int i = 0; i < kAhead - 1; ++i) ask(i);
-  float acc[TM][NM][4];
+  uint64_t acc[TM][NM][2];               // columns 0 and 1, 2 and 3 of the thread's
 #pragma unroll
   for (int t = 0; t < TM; ++t)
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[t][m][j] = 0.f;
+      for (int j = 0; j < 2; ++j) acc[t][m][j] = 0;
   int i = 0;
   for (int r0 = 0; r0 < depth; r0 += kXRows) {
     const int rows = depth - r0 < kXRows ? depth - r0 : kXRows;
@@ -327,14 +343,14 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
         for (int t = 0; t < TM; ++t) xv[t] = xr[t];
       }
 #pragma unroll
-      for (int t = 0; t < TM; ++t)
+      for (int t = 0; t < TM; ++t) {
+        const uint64_t xx = pack2(xv[t], xv[t]);
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-          acc[t][m][0] = fmaf(xv[t], w[m].x, acc[t][m][0]);
-          acc[t][m][1] = fmaf(xv[t], w[m].y, acc[t][m][1]);
-          acc[t][m][2] = fmaf(xv[t], w[m].z, acc[t][m][2]);
-          acc[t][m][3] = fmaf(xv[t], w[m].w, acc[t][m][3]);
+          fma2(acc[t][m][0], xx, pack2(w[m].x, w[m].y));
+          fma2(acc[t][m][1], xx, pack2(w[m].z, w[m].w));
         }
+      }
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -348,7 +364,8 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
     for (int m = 0; m < NM; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float v = acc[t][m][j];
+        const float2 pair = unpack2(acc[t][m][j / 2]);
+        float v = j % 2 ? pair.y : pair.x;
 #pragma unroll
         for (int o = CT; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane < CT) red[warp * L + (t * NM + m) * C + tile_col<CT, WIDE>(ct, j)] = v;
