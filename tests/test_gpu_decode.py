@@ -100,6 +100,13 @@ def test_f32_shapes(sizes):
     run(small_shape("s", N=N, H=H, E=E, K=K, F=F, dtype="f32"), seed=4)
 
 
+@pytest.mark.parametrize("F", [63, 64, 205, 208, 443, 444])
+@pytest.mark.parametrize("H", [188, 384, 388])
+def test_f32_tile_widths(H, F):
+    """Every pair of widths that gate and up, and down, may take, with and without aligned rows."""
+    run(small_shape("w", N=64, H=H, E=30, K=6, F=F, dtype="f32"), seed=6)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("skew", [("zipf", 1.0), ("normal", 3.0), ("zipf", 6.0)])
 def test_skewed_routing(dtype, skew):
