@@ -279,7 +279,8 @@ def moe_add_rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None
     """h = x + residual (h = x without one), y = h / sqrt(mean(h^2) + eps) * weight; returns (y, h).
 
     x, residual [N, H], weight [H].  y and h may be given, also to work in place
-    (h = residual or x, y = x or residual, two different buffers).
+    (h = residual or x, y = x or residual, two different buffers).  Without a residual and with y
+    over x, h is gone once y is there: None is returned for it, so it cannot be taken for the backward's h.
     """
     shape, dtype, dev = x.shape, x.dtype, x.get_device()
     if len(shape) != 2:
@@ -300,8 +301,11 @@ def moe_add_rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None
         if h is None:
             h = torch.empty_like(x)
         ph = _arg("h", h, shape, dtype, dev)
-    _call_on(dev, "moe_add_rms_norm", px, pr, pw, N, H, dt, eps, ph, _arg("y", y, shape, dtype, dev))
-    return y, (x if residual is None else h)
+    py = _arg("y", y, shape, dtype, dev)
+    _call_on(dev, "moe_add_rms_norm", px, pr, pw, N, H, dt, eps, ph, py)
+    if residual is None:
+        h = x if py != px or N == 0 else None
+    return y, h
 
 
 def moe_add_rms_norm_bwd(dy, h, weight, dh=None, eps: float = 1e-6, dx=None, dweight=None, ws=None):

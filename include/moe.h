@@ -371,7 +371,8 @@ moe_status moe_layer_decode(const void* x, const void* W_r, const void* W1, cons
  * the normalisation run in fp32.
  *   x, residual, h, y [N,H]; weight [H] (all dt); eps >= 0.
  * In place: h may be residual or x, y may be x or residual (not both outputs
- * the same buffer); any other overlap is undefined.
+ * the same buffer); any other overlap is undefined.  Without a residual, y over x
+ * leaves no h: the backward needs the x that y has replaced.
  * H: a multiple of 8 up to 16384 (bf16), of 4 up to 8192 (fp32). */
 moe_status moe_add_rms_norm(const void* x, const void* residual, const void* weight, int32_t N, int32_t H,
                             moe_dtype dt, float eps, void* h, void* y, moe_stream_t stream);

@@ -216,3 +216,26 @@ def test_replays_from_a_graph_and_on_another_stream():
         torch.cuda.synchronize()
         for got, ref in zip((y, h, dx, dw), want):
             assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_in_place_without_a_residual_has_no_h_to_give(dtype):
+    """h is x there, and y has taken its place: what came back as h would be y, and the
+    backward pass of it another function's."""
+    dt = DT[dtype]
+    x, w, dy = rand((37, 256), dt, 1), rand((256,), dt, 2), rand((37, 256), dt, 3)
+    keep = x.clone()
+    y, h = moe.moe_add_rms_norm(x, w, eps=EPS, y=x)
+    assert y is x and h is None
+    check_forward(y, keep, keep, None, w)
+    x = keep.clone()
+    y, h = moe.moe_add_rms_norm(x, w, eps=EPS, y=x.view(37, 256))      # another tensor of the same memory
+    assert h is None and torch.equal(x, y)
+    y, h = moe.moe_add_rms_norm(keep, w, eps=EPS, y=torch.empty_like(keep))
+    assert h is keep
+    dx, dw = moe.moe_add_rms_norm_bwd(dy, h, w, eps=EPS)
+    check_backward(dx, dw, dy, keep, w, None)
+    r = rand((37, 256), dt, 4)
+    x = keep.clone()
+    y, h = moe.moe_add_rms_norm(x, w, residual=r, eps=EPS, y=x)        # with a residual h has a buffer of its own
+    check_forward(y, h, keep, r, w)
