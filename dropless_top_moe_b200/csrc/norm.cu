@@ -399,12 +399,12 @@ moe_status norm_bwd(const void* dy, const void* h, const void* w, const void* dh
 
 inline bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-// Two buffers that share memory without being the same one: a row's block
-// would overwrite rows that others still have to read.
-bool cross(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || (a == b && na == nb)) return false;
-  return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  return a && b && (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
 }
+// Two [N,H] buffers that share memory without being the same one: a row's block
+// would overwrite rows that others still have to read.
+bool cross(const void* a, const void* b, size_t n) { return a != b && overlap(a, n, b, n); }
 
 }  // namespace
 }  // namespace moe
@@ -423,8 +423,8 @@ moe_status moe_add_rms_norm(const void* x, const void* residual, const void* wei
   if (N == 0) return MOE_OK;
   if (!residual) h = nullptr;
   const size_t row = (size_t)H * (dt == MOE_F32 ? 4 : 2), all = row * N;
-  if (h == y || cross(h, all, y, all) || cross(h, all, weight, row) || cross(y, all, weight, row) ||
-      cross(h, all, x, all) || cross(h, all, residual, all) || cross(y, all, x, all) || cross(y, all, residual, all))
+  if (overlap(h, all, y, all) || overlap(h, all, weight, row) || overlap(y, all, weight, row) ||
+      cross(h, x, all) || cross(h, residual, all) || cross(y, x, all) || cross(y, residual, all))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   if (dt == MOE_F32)
@@ -450,10 +450,10 @@ moe_status moe_add_rms_norm_bwd(const void* dy, const void* h, const void* weigh
   if (!ws || ws_bytes < moe_add_rms_norm_bwd_workspace_size(N, H, dt)) return MOE_ERR_WORKSPACE;
   if (!al16(ws)) return MOE_ERR_INVALID_ARG;
   const size_t row = (size_t)H * (dt == MOE_F32 ? 4 : 2), all = row * N;
-  if (N > 0 && (cross(dx, all, dy, all) || cross(dx, all, h, all) || cross(dx, all, dh, all) ||
-                cross(dx, all, weight, row) || cross(dx, all, dweight, row) || cross(dweight, row, dy, all) ||
-                cross(dweight, row, h, all) || cross(dweight, row, dh, all) || dweight == weight ||
-                cross(dweight, row, weight, row)))
+  if (overlap(dweight, row, weight, row)) return MOE_ERR_INVALID_ARG;
+  if (N > 0 && (cross(dx, dy, all) || cross(dx, h, all) || cross(dx, dh, all) || overlap(dx, all, weight, row) ||
+                overlap(dx, all, dweight, row) || overlap(dweight, row, dy, all) || overlap(dweight, row, h, all) ||
+                overlap(dweight, row, dh, all)))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   if (N == 0) {   // no rows: an empty sum

@@ -371,7 +371,7 @@ moe_status moe_layer_decode(const void* x, const void* W_r, const void* W1, cons
  * the normalisation run in fp32.
  *   x, residual, h, y [N,H]; weight [H] (all dt); eps >= 0.
  * In place: h may be residual or x, y may be x or residual (not both outputs
- * the same buffer); any other overlap is undefined.  Without a residual, y over x
+ * the same buffer); any other overlap is MOE_ERR_INVALID_ARG.  Without a residual, y over x
  * leaves no h: the backward needs the x that y has replaced.
  * H: a multiple of 8 up to 16384 (bf16), of 4 up to 8192 (fp32). */
 moe_status moe_add_rms_norm(const void* x, const void* residual, const void* weight, int32_t N, int32_t H,
@@ -382,7 +382,8 @@ moe_status moe_add_rms_norm(const void* x, const void* residual, const void* wei
  *   dweight = round(sum_n dy[n] * xhat[n])    (fixed order, fp32)
  * dh [N,H] is the gradient that reaches h past the norm (the residual stream),
  * NULL for none; dx is the gradient of x and of residual alike.
- *   dy, h, dh, dx [N,H]; weight, dweight [H] (all dt).  dx may be dy, h or dh.
+ *   dy, h, dh, dx [N,H]; weight, dweight [H] (all dt).  dx may be dy, h or dh;
+ *   any other overlap of an output is MOE_ERR_INVALID_ARG.
  *   N = 0: dweight is zeroed.  H as above.
  * ws: moe_add_rms_norm_bwd_workspace_size bytes (never less for more rows; 0
  * for a shape the call would reject); it needs no moe_workspace_init. */

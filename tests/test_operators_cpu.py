@@ -144,3 +144,18 @@ def test_binding_checks_the_few_token_layers_tensors():
         moe.MoEDecodeLayer(8, 100, 4, 2, 256)
     with pytest.raises(TypeError, match="dtype"):
         moe.MoEDecodeLayer(8, 128, 4, 2, 256, dtype=torch.float16)
+
+
+def test_norm_refuses_shared_memory_in_a_single_row_too(lib):
+    """A row of weight or dweight is as large as x or dx are when there is one row."""
+    def fwd(N, x=A, r=B, w=C, h=D, y=E_):
+        return lib.moe_add_rms_norm(x, r, w, N, 128, MOE_BF16, 1e-6, h, y, None)
+
+    def bwd(N, dy=A, h=B, w=C, dh=None, dx=D, dw=E_):
+        return lib.moe_add_rms_norm_bwd(dy, h, w, dh, N, 128, MOE_BF16, 1e-6, dx, dw, 6 * A, BIG, None)
+    for N in (2, 1):
+        assert fwd(N, h=C) == INV and fwd(N, y=C) == INV, N
+        assert bwd(N, dw=D) == INV, N                               # dx and dweight the same
+        assert bwd(N, dx=C) == INV and bwd(N, dw=C) == INV, N
+        assert bwd(N, dw=A) == INV and bwd(N, dw=B) == INV and bwd(N, dh=7 * A, dw=7 * A) == INV, N
+    assert bwd(0, dw=C) == INV
