@@ -22,10 +22,11 @@
 // 1 token 2048/64/6/1408 (104 MB) 30 us, of which 16 are the weights.
 //
 // The activations pass to the down product as two bf16 numbers, the rounded value
-// and what the rounding left (kSplitTokens tokens a slot at most; beyond, the value
-// alone): as further columns of the same MMAs they cost 1 % at most, and y is as
-// exact as with fp32 activations (relative error 0.0017, its own rounding; 0.0024
-// without).
+// and what the rounding left, and y is as exact as with fp32 activations (relative
+// error 0.0017, its own rounding; 0.0024 without).  Up to kSplitTokens tokens a slot both
+// are columns of the same MMAs (1 % at most); beyond, where those columns would pass the
+// accumulators' 128, a second MMA adds the rests to the same sums, so that a token's
+// precision does not depend on how many others share its expert.
 //
 // With a few tokens the time is a chain of latencies, and the hand-over between the
 // phases the longest of them: written, fenced, counted, added up, written, fenced,
@@ -134,10 +135,10 @@ __device__ __forceinline__ Ticket read_ticket(int v, const Line& up, const Line&
 
 __device__ __forceinline__ int round16(int v) { return (v + 15) & ~15; }
 __device__ __forceinline__ int round8(int v) { return (v + 7) & ~7; }
-// Rows of the down product's token tile: the rounded activations from row 0 on, what
-// the rounding left of them from row round8(cnt) on.
-__device__ __forceinline__ bool splits(int cnt) { return cnt <= kSplitTokens; }
-__device__ __forceinline__ int down_rows(int cnt) { return splits(cnt) ? 2 * round8(cnt) : round16(cnt); }
+// The down product's token tile: the rounded activations from row 0 on, what the
+// rounding left of them from row down_half(cnt) on; one_mma: columns of one MMA.
+__device__ __forceinline__ bool one_mma(int cnt) { return cnt <= kSplitTokens; }
+__device__ __forceinline__ int down_half(int cnt) { return one_mma(cnt) ? round8(cnt) : round16(cnt); }
 // What rounding v to bf16 leaves; nothing of a value that is not finite as bf16.
 __device__ __forceinline__ float rest_of(float v) {
   const float r = v - __bfloat162float(__float2bfloat16_rn(v));
@@ -424,7 +425,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         const Piece pc = piece_at(l, pos, end);
         const int u = pc.tile / l.nj;
         const int e = sm.plan.expert[u], r0 = sm.plan.off[u], cnt = sm.plan.off[u + 1] - r0;
-        const int rows = k.up ? round16(cnt) : down_rows(cnt);
+        const int rows = k.up ? round16(cnt) : 2 * down_half(cnt);
         int g0 = a.N, g1 = a.N, g2 = a.N, g3 = a.N;        // rows past the last token read as zeros
         if (DIRECT && k.up && builder != 0) {
           for (int i = 0; i < pc.len; ++i)
@@ -540,8 +541,8 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           if (k.up) {
             if (4 * lane < rows) tma_gather4(dst + lane * 512, &p.tx, bar(sm.full[stage]), kcol, g0, g1, g2, g3);
           } else {
-            // box b: rows 8 b on; the second half of a split slot's boxes are what the rounding left
-            const int half = splits(cnt) ? rows / 16 : 16;
+            // box b: rows 8 b on; the second half of the boxes are what the rounding left
+            const int half = rows / 16;
             const int row = lane < half ? r0 + 8 * lane : a.N * a.K + r0 + 8 * (lane - half);
             if (8 * lane < rows) tma_load_2d(dst + lane * 1024, &p.tact, bar(sm.full[stage]), kcol, row);
           }
@@ -581,7 +582,8 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           const Piece pc = piece_at(l, pos, end);
           const int u = pc.tile / l.nj;
           const int cnt = sm.plan.off[u + 1] - sm.plan.off[u];
-          const uint32_t idesc = idesc_bf16(128, k.up ? round16(cnt) : down_rows(cnt), true, false);
+          const bool two = !DIRECT && !k.up && !one_mma(cnt);
+          const uint32_t idesc = idesc_bf16(128, k.up || two ? round16(cnt) : 2 * down_half(cnt), true, false);
           ok = mbar_wait_bounded(bar(sm.tempty[acc]), acc_phase ^ 1u, abort_flag, a.status, kTimeoutNs);
           if (!ok) break;
           tc_fence_after();
@@ -594,6 +596,12 @@ decode_umma_kernel(const __grid_constant__ Params p) {
 #pragma unroll
             for (int kk = 0; kk < kKB / 16; ++kk)
               mma_bf16(d, desc_mn_sw128(sa + kk * 2048, 8192), desc_k_sw128(sb + kk * 32), idesc, (i | kk) != 0 ? 1u : 0u);
+            if (two) {
+              const uint32_t sr = sb + down_half(cnt) * 128;
+#pragma unroll
+              for (int kk = 0; kk < kKB / 16; ++kk)
+                mma_bf16(d, desc_mn_sw128(sa + kk * 2048, 8192), desc_k_sw128(sr + kk * 32), idesc, 1u);
+            }
             mma_commit(bar(sm.empty[stage]));
             if (++stage == p.stages) { stage = 0; phase ^= 1u; }
           }
@@ -649,7 +657,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         const uint32_t d = tmem + acc * 256 + lanes;
         const int a0 = pc.tile * l.kc;
         float* part = (k.up ? p.part_up : p.part_down) + entry * l.entry(k.t, a0) + et;
-        const int rest = !k.up && splits(cnt) ? round8(cnt) : 0;    // columns from a value to its rest's
+        const int rest = !k.up && one_mma(cnt) ? down_half(cnt) : 0;    // columns from a value to its rest's
         for (int c = 0; c < cnt; c += 16) {
           uint32_t v0[16], v1[16];
           tmem_ld_16(d + c, v0);
@@ -837,8 +845,9 @@ moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, floa
   p.part_up = part_up;
   p.part_down = part_down;
   p.tile_cnt = tile_cnt;
-  p.b_bytes = (a.N <= kSplitTokens ? 2 * (int)round_up(a.N, 8) : 2 * kSplitTokens) * 128;
-  static_assert(2 * kSplitTokens >= kMaxTokens, "the widest slot's rows");
+  // both halves of the widest slot, and the up product's round16 rows of it
+  p.b_bytes = 2 * (int)round_up(a.N, a.N <= kSplitTokens ? 8 : 16) * 128;
+  static_assert(2 * kSplitTokens <= 128 && kMaxTokens <= 128, "an accumulator's columns");
   p.stages = kSmemData / (kABytes + p.b_bytes);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   if (!map3(&p.tw1, a.W1, a.F, a.H, a.E, 64, 3) || !map3(&p.tw3, a.W3, a.F, a.H, a.E, 64, 3) ||

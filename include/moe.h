@@ -346,10 +346,10 @@ moe_status moe_sum_rank_ordered(const void* shards, int32_t n_ranks, int64_t num
  *   x, y [N,H] (dt), N <= moe_decode_max_tokens(); top_experts [N,K] int32;
  *   weights [N,K] float32.  y may be x; no other overlap.
  * Sums run in fp32 and y is rounded once: expert outputs stay in fp32, and bf16
- * layers carry the activations as two bf16 numbers (one for an expert with more
- * than 64 of the tokens), so y can differ in the last bits from moe_layer_fwd's.  The same inputs give the
- * same bits on every call, and a token's outputs depend on its own row only up
- * to the order of fp32 sums.  A NaN logit ranks like -infinity.
+ * layers carry the activations as two bf16 numbers, so y can differ in the last
+ * bits from moe_layer_fwd's.  The same inputs give the same bits on every call,
+ * and a token's outputs depend on its own row only, up to the order of fp32 sums.
+ * A NaN logit ranks like -infinity.
  * Shapes: K <= E <= 256, K <= 32; bf16: H and F multiples of 128; fp32: H a
  * multiple of 4, any F; H, F <= 65536.
  * ws: moe_layer_decode_workspace_size bytes for this N or a larger one, the

@@ -268,3 +268,24 @@ def test_serving_and_training_steps_together():
     after = float(sum(t.double().square().sum() for t in grads)) ** 0.5
     assert abs(after - 1.0) <= 2.0 ** -8 + 1e-6            # each element rounds to bf16 once
     assert full.status() == 0 and few.status() == 0 and bool(torch.isfinite(dx).all())
+
+
+@pytest.mark.parametrize("H,F", [(128, 128), (256, 512), (1024, 1280)])
+@pytest.mark.parametrize("E", [1, 2])
+def test_precision_does_not_depend_on_the_other_tokens(E, H, F):
+    """The same rows while their experts' tokens grow past 64: every count has the bound of
+    activations carried as two numbers (2^-16), which reference() gives to parts of 64."""
+    shape = small_shape("split", N=128, H=H, E=E, K=E, F=F)
+    c = make_case(shape, seed=20, with_dy=False)
+    layer = moe.MoEDecodeLayer(128, H, E, E, F)
+    ref = om.route(c["x_cpu"], c["W_r_cpu"], E)
+    ids = torch.as_tensor(np.asarray(ref["top_experts"]), device="cuda").long()
+    w = torch.as_tensor(np.asarray(ref["weights"]), device="cuda")
+    parts = [{k: (v[s:s + 64] if k in ("x", "x_cpu") else v) for k, v in c.items()} for s in (0, 64)]
+    y64, tol = (torch.cat(t) for t in zip(*(reference(p, ids[s:s + 64], w[s:s + 64], E)
+                                            for p, s in zip(parts, (0, 64)))))
+    for n in (64, 65, 72, 80, 81, 96, 97, 112, 127, 128):
+        y = layer.forward(c["x"][:n], c["W_r"], c["W1"], c["W3"], c["W2"])
+        err = (y.double() - y64[:n]).abs()
+        assert layer.status() == 0
+        assert bool((err <= tol[:n]).all()), (n, float((err / tol[:n]).max()))
