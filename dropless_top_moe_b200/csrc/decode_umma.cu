@@ -76,8 +76,9 @@ struct Params {
   float* part_down;
   int* tile_cnt;               // [slots][F / 128] pieces that have arrived, zeroed by the router
   RouteCut cut;
-  int stages;
-  int b_bytes;                 // of a stage: the most rows of 128 bytes that N tokens take
+  // of the ring, [1] where a slot holds more than kSplitTokens tokens
+  int stages[2];
+  int b_bytes[2];              // of a stage: the most rows of 128 bytes that its tokens take
 };
 
 // A phase's line of units and its cut into tickets of q units.
@@ -276,12 +277,11 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   const Args& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t stage_bytes = kABytes + p.b_bytes;
   volatile int* abort_flag = &sm.abort;
   auto bar = [](const uint64_t& b) { return smem_u32(&b); };
 
   if (tid == 0) {
-    for (int i = 0; i < p.stages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(bar(sm.full[i]), 2);         // the weights' producer and the tokens'
       mbar_init(bar(sm.empty[i]), 2);        // both MMA warps
     }
@@ -319,11 +319,17 @@ decode_umma_kernel(const __grid_constant__ Params p) {
   } else {
     build_plan(sm.plan, a.top, a.N, a.K, a.E, (int)blockDim.x);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sm.tmem;
   const int slots = sm.plan.slots;
+  // Wider stages, and one fewer of them from 81 tokens on, only where a slot needs them: three stages
+  // for every such call cost 3 % of those bound by HBM (128 tokens 4096/64/4/2048: 524 us with four,
+  // 540 with three).  With all 128 tokens on one expert 4096/1/1/8192 the three and the second
+  // MMAs cost 143 us against the 127 of activations rounded to one number.
+  tc_fence_before();
+  const int wide = __syncthreads_or(!DIRECT && tid < slots && !one_mma(sm.plan.off[tid + 1] - sm.plan.off[tid]));
+  tc_fence_after();
+  const int stages = p.stages[wide != 0];
+  const uint32_t stage_bytes = kABytes + p.b_bytes[wide != 0];
+  const uint32_t tmem = sm.tmem;
   // a quarter of the mean tokens a slot (60 tokens on each of two experts 2432/640: 77 us
   // without, 54 with), and eight units, so that short tiles stay whole (61 tokens
   // 256/6/4/1024: 38 us without, 30 with); four in the direct variant, where cuts cost less
@@ -380,7 +386,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
             if (lane < 4)
               tma_load_3d(base + stage * stage_bytes + lane * 8192, m, bar(sm.full[stage]), c, (pc.k0 + i) * kKB, e);
             ++issued;
-            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
           }
           pos += pc.len;
         }
@@ -392,8 +398,8 @@ decode_umma_kernel(const __grid_constant__ Params p) {
     }
     if (lane == 0) {
       // the copies in flight land before the block leaves, also after a wait gave up
-      for (int i = 0; i < p.stages && i < issued; ++i) {
-        if (stage-- == 0) { stage = p.stages - 1; phase ^= 1u; }
+      for (int i = 0; i < stages && i < issued; ++i) {
+        if (stage-- == 0) { stage = stages - 1; phase ^= 1u; }
         const uint64_t t0 = globaltimer();
         while (!mbar_try_wait(bar(sm.full[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
       }
@@ -429,7 +435,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
         int g0 = a.N, g1 = a.N, g2 = a.N, g3 = a.N;        // rows past the last token read as zeros
         if (DIRECT && k.up && builder != 0) {
           for (int i = 0; i < pc.len; ++i)
-            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
           pos += pc.len;
           continue;
         }
@@ -527,7 +533,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(sm.full[stage]));
             }
-            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
             continue;
           }
           if (lane == 0) {
@@ -547,14 +553,14 @@ decode_umma_kernel(const __grid_constant__ Params p) {
             if (8 * lane < rows) tma_load_2d(dst + lane * 1024, &p.tact, bar(sm.full[stage]), kcol, row);
           }
           ++issued;
-          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+          if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
         pos += pc.len;
       }
     }
     if (lane == 0) {
-      for (int i = 0; i < p.stages && i < issued; ++i) {
-        if (stage-- == 0) { stage = p.stages - 1; phase ^= 1u; }
+      for (int i = 0; i < stages && i < issued; ++i) {
+        if (stage-- == 0) { stage = stages - 1; phase ^= 1u; }
         const uint64_t t0 = globaltimer();
         while (!mbar_try_wait(bar(sm.full[stage]), phase) && globaltimer() - t0 < 50000000ull) {}
       }
@@ -603,7 +609,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
                 mma_bf16(d, desc_mn_sw128(sa + kk * 2048, 8192), desc_k_sw128(sr + kk * 32), idesc, 1u);
             }
             mma_commit(bar(sm.empty[stage]));
-            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
           }
           if (!ok) break;
           mma_commit(bar(sm.tfull[acc]));
@@ -846,15 +852,22 @@ moe_status experts_umma(const Args& a, const RouteCut& cut, float* part_up, floa
   p.part_down = part_down;
   p.tile_cnt = tile_cnt;
   // both halves of the widest slot, and the up product's round16 rows of it
-  p.b_bytes = 2 * (int)round_up(a.N, a.N <= kSplitTokens ? 8 : 16) * 128;
+  const int narrow = a.N < kSplitTokens ? a.N : kSplitTokens;
+  p.b_bytes[0] = 2 * (int)round_up(narrow, 8) * 128;
+  p.b_bytes[1] = 2 * (int)round_up(a.N, 16) * 128;
   static_assert(2 * kSplitTokens <= 128 && kMaxTokens <= 128, "an accumulator's columns");
-  p.stages = kSmemData / (kABytes + p.b_bytes);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  size_t smem = 0;
+  for (int i = 0; i < 2; ++i) {
+    p.stages[i] = kSmemData / (kABytes + p.b_bytes[i]);
+    if (p.stages[i] > kMaxStages) p.stages[i] = kMaxStages;
+    const size_t ring = (size_t)p.stages[i] * (kABytes + p.b_bytes[i]) + 1024;
+    if (smem < ring) smem = ring;
+    if (a.N <= kSplitTokens) break;      // no slot is wider
+  }
   if (!map3(&p.tw1, a.W1, a.F, a.H, a.E, 64, 3) || !map3(&p.tw3, a.W3, a.F, a.H, a.E, 64, 3) ||
       !map3(&p.tw2, a.W2, a.H, a.F, a.E, 64, 3) || !map3(&p.tx, a.x, a.H, a.N, 1, 1, 2) ||
       !map3(&p.tact, a.act, a.F, (uint64_t)2 * a.N * a.K, 1, 8, 2))
     return MOE_ERR_CUDA;
-  const size_t smem = (size_t)p.stages * (kABytes + p.b_bytes) + 1024;
   static bool set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
