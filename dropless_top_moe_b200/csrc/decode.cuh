@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "decode_line.cuh"
 #include "kernels.cuh"
 #include "pdl.cuh"
 #include "umma.cuh"
@@ -13,7 +14,6 @@
 namespace moe {
 namespace decode {
 
-constexpr int kBlocks = 148;                // of the expert kernels: one an SM
 constexpr int kMaxTokens = 128;
 static_assert(kMaxTokens <= kBlocks, "a block's share of y lies in two rows");
 constexpr int kMaxExperts = 256;

@@ -61,7 +61,6 @@ constexpr int kKB = 64;                     // rows of a unit
 constexpr int kABytes = 4 * 8192;           // four 64 x 64 weight boxes
 constexpr int kMaxStages = 6;
 constexpr int kRing = 8;                    // tickets in flight in a block
-constexpr int kLongUnits = 16;
 constexpr int kUpTickets = 2, kDownTickets = 4;    // a block, on long lines
 constexpr int kSmemData = 210 * 1024;
 constexpr int kSplitTokens = 64;
@@ -81,47 +80,6 @@ struct Params {
   int b_bytes[2];              // of a stage: the most rows of 128 bytes that its tokens take
 };
 
-// A phase's line of units and its cut into tickets of q units.
-struct Line {
-  int nj, kc;      // tiles of a slot, units of a tile
-  int units, q, tickets;
-  __device__ __forceinline__ int start(int t) const { return t * q < units ? t * q : units; }
-  __device__ __forceinline__ int ticket_of(int u) const { return u / q; }
-  // Partial-sum entry of ticket t's piece of the tile that starts at unit a.
-  __device__ __forceinline__ int entry(int t, int a) const { return 2 * t + (t * q >= a ? 0 : 1); }
-};
-// One ticket a block, or `per_block` of them where that leaves two a block at least
-// kLongUnits units each.  More tickets even out the blocks' ends, and cut tiles
-// into more pieces: 2 a block for gate/up and 4 for down measured best (2 and 2: 208 us
-// for 8 tokens 4096/64/4/2048, 200 with 2 and 4, 202 with 4 and 4; a line
-// ending in shorter tickets gained nothing over that).
-__host__ __device__ __forceinline__ int ticket_count(int64_t units, int per_block) {
-  return units >= (int64_t)kBlocks * 2 * kLongUnits ? per_block * kBlocks : kBlocks;
-}
-// A ticket is at least `least` units, or a tile: with many tokens a piece's partial sums
-// cost more than its weights.
-__device__ __forceinline__ Line make_line(int slots, int nj, int kc, int per_block, int least) {
-  Line l;
-  l.nj = nj;
-  l.kc = kc;
-  l.units = slots * nj * kc;
-  const int most = ticket_count(l.units, per_block);
-  l.q = (l.units + most - 1) / most;
-  if (l.q < least) l.q = least < kc ? least : kc;
-  l.tickets = (l.units + l.q - 1) / l.q;
-  return l;
-}
-// A ticket's next piece: units [pos, pos + len) of one tile.
-struct Piece {
-  int tile, k0, len;
-};
-__device__ __forceinline__ Piece piece_at(const Line& l, int pos, int end) {
-  Piece p;
-  p.tile = pos / l.kc;
-  p.k0 = pos - p.tile * l.kc;
-  p.len = l.kc - p.k0 < end - pos ? l.kc - p.k0 : end - pos;
-  return p;
-}
 struct Ticket {
   bool up, stop;
   int t;
@@ -831,7 +789,8 @@ bool map3(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2
 
 }  // namespace
 
-// Buffers of partial sums: no more tickets than the line of every expert that can be used has.
+// Buffers of partial sums: the tickets of a line that cuts tiles are no more than ticket_count gives
+// for the line of every expert that can be used (make_line).
 static int64_t line_units(int N, int K, int E, int nj, int kc) {
   return (N * (int64_t)K < E ? N * (int64_t)K : E) * nj * kc;
 }

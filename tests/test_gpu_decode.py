@@ -289,3 +289,11 @@ def test_precision_does_not_depend_on_the_other_tokens(E, H, F):
         err = (y.double() - y64[:n]).abs()
         assert layer.status() == 0
         assert bool((err <= tol[:n]).all()), (n, float((err / tol[:n]).max()))
+
+
+@pytest.mark.parametrize("sizes", [(128, 128, 4, 2, 1280), (100, 128, 16, 8, 4096), (96, 4096, 12, 6, 128),
+                                   (128, 128, 8, 8, 8192)], ids=str)
+def test_many_tokens_on_many_short_tiles(sizes):
+    """Tiles of two units, shorter than the length asked of a ticket for that many tokens."""
+    N, H, E, K, F = sizes
+    run(small_shape("short", N=N, H=H, E=E, K=K, F=F), seed=28)

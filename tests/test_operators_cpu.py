@@ -1,6 +1,7 @@
 """Refusals of the norm, clipping and few-token entry points (CPU only: the
 checks run before any device work, so pointers are never dereferenced)."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -159,3 +160,19 @@ def test_norm_refuses_shared_memory_in_a_single_row_too(lib):
         assert bwd(N, dx=C) == INV and bwd(N, dw=C) == INV, N
         assert bwd(N, dw=A) == INV and bwd(N, dw=B) == INV and bwd(N, dh=7 * A, dw=7 * A) == INV, N
     assert bwd(0, dw=C) == INV
+
+
+def test_few_token_tickets_cover_their_line(tmp_path):
+    """tests/c_api/decode_line.cpp: the plain arithmetic of decode_line.cuh, run on the CPU."""
+    import shutil
+    import subprocess
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "decode_line")
+    subprocess.run([cxx, "-std=c++17", "-O2", "-Wall", "-Wextra", "-Werror", "-x", "c++",
+                    "-I", os.path.join(root, "dropless_top_moe_b200", "csrc"),
+                    os.path.join(root, "tests", "c_api", "decode_line.cpp"), "-o", exe], check=True)
+    res = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert res.returncode == 0, res.stdout[-2000:]
