@@ -22,6 +22,8 @@
 //
 // Measured: 3.2 GB of bf16 gradients 1.44 ms (9.7 GB moved: 6.7 TB/s), 288 MB in 60
 // tensors 139 us; 16 KB chunks and two thirds of the blocks took 1.60 ms, 150 us.
+#include <float.h>
+
 #include <algorithm>
 #include <new>
 #include <utility>
@@ -191,6 +193,18 @@ __device__ __forceinline__ void chunk_scale(const T* g, T* out, int64_t numel, i
   }
 }
 
+// The same for a factor below a float's normal range, which would keep few of its bits there while
+// g * f may well be normal: the products in double, an element at a time (nothing that a
+// training step meets, and no registers for the vectors above).
+template <typename T>
+__device__ __forceinline__ void chunk_scale_tiny(const T* g, T* out, int64_t numel, int chunk, bool last, double f) {
+  constexpr int64_t E = (int64_t)kChunkVec * Vec<T>::N;
+  const int64_t end = last ? numel : (chunk + 1) * E;
+#pragma unroll 1
+  for (int64_t at = chunk * E + threadIdx.x; at < end; at += kClipThreads)
+    out[at] = from_f<T>((float)((double)to_f<T>(g[at]) * f));
+}
+
 // The norm from the blocks' sums (in a fixed order, the same in every block),
 // then the scaling.  copy: the outputs are other buffers, written for f = 1 too.
 template <int M>
@@ -217,7 +231,12 @@ grad_scale_kernel(const __grid_constant__ ClipTable<M> tab, const double* __rest
     const int i = tensor_of(tab, c);
     const ClipTensor& t = tab.t[i];
     const bool last = c + 1 == (i + 1 < tab.count ? tab.t[i + 1].first : tab.chunks);
-    if (t.dt == MOE_F32)
+    if (f < FLT_MIN) {
+      if (t.dt == MOE_F32)
+        chunk_scale_tiny((const float*)t.g, (float*)t.out, t.numel, c - t.first, last, r);
+      else
+        chunk_scale_tiny((const __nv_bfloat16*)t.g, (__nv_bfloat16*)t.out, t.numel, c - t.first, last, r);
+    } else if (t.dt == MOE_F32)
       chunk_scale((const float*)t.g, (float*)t.out, t.numel, c - t.first, last, f);
     else
       chunk_scale((const __nv_bfloat16*)t.g, (__nv_bfloat16*)t.out, t.numel, c - t.first, last, f);

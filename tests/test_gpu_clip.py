@@ -183,3 +183,24 @@ def test_the_data_parallel_reduction_clips(tmp_path):
         check(allreduce_grads(grads, max_norm=1.5), grads, keep, 1.5)
     finally:
         dist.destroy_process_group()
+
+
+def test_a_factor_below_the_smallest_normal_float():
+    """max_norm / norm below 2^-126: the factor has few bits as a float, and the scaled gradients do not."""
+    for dt in (torch.float32, torch.bfloat16):
+        for scale, limit in ((1e36, 1e-2), (1e37, 1e-6), (3e36, 2e-20)):
+            grads = [rand((5000,), dt, 1, scale), rand((77,), dt, 2, scale)]
+            keep = [g.clone() for g in grads]
+            outs = [torch.empty_like(g) for g in grads]
+            norm = moe.moe_clip_grad_norm(grads, limit, outs=outs)
+            again = moe.moe_clip_grad_norm(grads, limit)                            # in place
+            n = norm64(keep)
+            assert torch.equal(norm, again)
+            # a norm past the largest float is infinity as a float
+            assert abs(float(norm) - n) <= 17 * U * n or (n > torch.finfo(torch.float32).max and math.isinf(float(norm)))
+            f = limit / (n + 1e-6)
+            assert f < 2.0 ** -126
+            for o, p, g in zip(outs, grads, keep):
+                want = g.double() * f
+                tol = want.abs() * (torch.finfo(dt).eps / 2 + 20 * U) + torch.finfo(dt).tiny
+                assert torch.equal(o, p) and bool(((o.double() - want).abs() <= tol).all())
