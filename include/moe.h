@@ -405,8 +405,10 @@ moe_status moe_add_rms_norm_bwd(const void* dy, const void* h, const void* weigh
  * grads[i]; two written ranges that overlap, or one that overlaps another
  * gradient, are MOE_ERR_INVALID_ARG.  Empty tensors are skipped; an empty
  * list has norm 0.
- * max_norm >= 0; infinity only takes the norm.  A norm of infinity gives
- * f = 0, a NaN norm makes every gradient NaN, as the formula has it: test *norm.
+ * max_norm >= 0; infinity only takes the norm.  f comes from the norm in double: of
+ * finite gradients whose norm passes the largest float *norm is infinity, and they are
+ * scaled by its value all the same.  An infinite gradient gives f = 0, a NaN makes
+ * every gradient NaN, as the formula has it: test *norm.
  * Sums run in fp32 over four 16-byte vectors and in double beyond, in a fixed order;
  * the norm is right whenever it is a float, also where squares are not.
  * Two launches for up to 768 tensors.  Capturable.

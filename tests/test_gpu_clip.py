@@ -204,3 +204,16 @@ def test_a_factor_below_the_smallest_normal_float():
                 want = g.double() * f
                 tol = want.abs() * (torch.finfo(dt).eps / 2 + 20 * U) + torch.finfo(dt).tiny
                 assert torch.equal(o, p) and bool(((o.double() - want).abs() <= tol).all())
+
+
+def test_a_norm_past_the_largest_float():
+    """The norm is written as infinity; finite gradients are scaled by its value all the same."""
+    grads = [torch.full((400,), 3e38, device="cuda"), torch.full((9,), -1e30, device="cuda")]
+    outs = [torch.empty_like(g) for g in grads]
+    n = norm64(grads)
+    assert n > torch.finfo(torch.float32).max
+    for limit in (1e3, 1.0):
+        assert math.isinf(float(moe.moe_clip_grad_norm(grads, limit, outs=outs)))
+        for o, g in zip(outs, grads):
+            want = g.double() * (limit / n)
+            assert bool(((o.double() - want).abs() <= want.abs() * 20 * U + torch.finfo(g.dtype).tiny).all())
