@@ -3,8 +3,8 @@
 //   out  = round(g * f),  f = min(1, max_norm / (norm + 1e-6)).
 // Two launches: one sums the squares into one double a block, the other adds those in
 // block order (so the norm, and with it every bit of the scaled gradients, is
-// the same on every run and on every rank that holds the same gradients) and
-// scales.  In place with f = 1 there is nothing to write and the second launch
+// the same on every run and on every rank that holds the same gradients, wherever
+// they lie in memory) and scales.  In place with f = 1 there is nothing to write and the second launch
 // returns after the sum.
 //
 // Bound by HBM: two reads and a write of every gradient, less what the second
@@ -13,8 +13,9 @@
 //
 // The tensors travel in the kernel's parameters (no copy to the device that a
 // captured graph would have to keep); a longer list takes several launches.
-// A tensor is cut into 16-byte vectors from its first 16-byte boundary on, in
-// chunks of kChunkVec vectors; the few elements before and after go one by one.
+// A tensor is cut into chunks of kChunkVec vectors of 16 bytes, counted from its first
+// element for the sum and from its first 16-byte boundary on for the scaling, where
+// the few elements before and after go one by one.
 //
 // Squares are summed in fp32 over kSumVec vectors, then in double.  An fp32 sum that
 // overflowed, or so small that squares may have underflowed, is taken again in
@@ -74,52 +75,109 @@ __device__ __forceinline__ int tensor_of(const ClipTable<M>& tab, int c) {
   return lo;
 }
 
+// The sum of squares goes by element index alone: vector i of a tensor is its elements
+// V i to V i + V - 1, wherever the tensor starts, so that two ranks that hold the same gradients
+// at other offsets from a 16-byte boundary have the same norm to the last bit.  A tensor off the
+// boundary pays two loads a vector for it (800 MB: the whole call 422 us for 385 in bf16, 394 for 380 in fp32).
+
+// kSumVec vectors of a thread in fp32, in double where that left the range.
+template <typename T>
+__device__ __forceinline__ double vec_squares(const uint4* v) {
+  constexpr int V = Vec<T>::N;
+  float s = 0.f;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < kSumVec; ++i) {
+    float f[V];
+    Vec<T>::to_float(v[i], f);
+    bits |= v[i].x | v[i].y | v[i].z | v[i].w;
+#pragma unroll
+    for (int j = 0; j < V; ++j) s = fmaf(f[j], f[j], s);
+  }
+  if ((s > 1e-30f && s < 1e38f) || bits == 0) return (double)s;
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < kSumVec; ++i) {
+    float f[V];
+    Vec<T>::to_float(v[i], f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum += (double)f[j] * (double)f[j];
+  }
+  return sum;
+}
+
+// A vector of a tensor that starts `off` bytes past a 16-byte boundary, out of the two aligned ones
+// that cover it.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (off & 8) {
+#pragma unroll
+    for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+  }
+  const int bits = (off & 2) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+template <typename T>
+__device__ __forceinline__ uint4 load_each(const T* p) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 4) w[j] = __ldg((const uint32_t*)p + j);
+    else w[j] = __ldg((const uint16_t*)p + 2 * j) | (uint32_t)__ldg((const uint16_t*)p + 2 * j + 1) << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Sum of the squares of one thread's part of a chunk.
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T* g, int64_t numel, int chunk, bool last) {
   constexpr int V = Vec<T>::N;
-  const int head = head_of(g, numel);
-  const int64_t nvec = (numel - head) / V;
-  const T* body = g + head;
-  const int64_t v0 = (int64_t)chunk * kChunkVec;
-  uint4 v[kChunkPer];
-#pragma unroll
-  for (int i = 0; i < kChunkPer; ++i) {
-    const int64_t at = v0 + threadIdx.x + i * kClipThreads;
-    v[i] = at < nvec ? ld_nc_v4(body + at * V) : make_uint4(0, 0, 0, 0);
-  }
+  const int64_t nvec = numel / V, left = nvec - (int64_t)chunk * kChunkVec;
+  const int n = left < kChunkVec ? (int)left : kChunkVec;       // vectors of this chunk
+  const int off = (int)((uintptr_t)g & 15u);
+  const char* from = (const char*)g + (int64_t)chunk * kChunkVec * 16;
+  const uint4 none = make_uint4(0, 0, 0, 0);
   double sum = 0.0;
+  uint4 v[kChunkPer];
+  if (off == 0) {
 #pragma unroll
-  for (int h = 0; h < kChunkPer; h += kSumVec) {
-    float s = 0.f;
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = h; i < h + kSumVec; ++i) {
-      float f[V];
-      Vec<T>::to_float(v[i], f);
-      bits |= v[i].x | v[i].y | v[i].z | v[i].w;
-#pragma unroll
-      for (int j = 0; j < V; ++j) s = fmaf(f[j], f[j], s);
+    for (int i = 0; i < kChunkPer; ++i) {
+      const int at = threadIdx.x + i * kClipThreads;
+      v[i] = at < n ? ld_nc_v4(from + (size_t)at * 16) : none;
     }
-    if ((s > 1e-30f && s < 1e38f) || bits == 0) {
-      sum += (double)s;
-    } else {
 #pragma unroll
-      for (int i = h; i < h + kSumVec; ++i) {
-        float f[V];
-        Vec<T>::to_float(v[i], f);
+    for (int h = 0; h < kChunkPer; h += kSumVec) sum += vec_squares<T>(v + h);
+  } else {
+    // A vector lies across two aligned ones, of which the second is in L1 as the next lane's first.  Those of
+    // the tensor's first and last vector reach past it: these two go element by element.
+    const int head = chunk == 0 ? 0 : -1, tail = left <= kChunkVec ? n - 1 : n;
+    const char* base = from - off;
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum += (double)f[j] * (double)f[j];
+    for (int h = 0; h < kChunkPer; h += kSumVec) {
+      uint4 o[kSumVec];
+#pragma unroll
+      for (int i = 0; i < kSumVec; ++i) {
+        const int at = threadIdx.x + (h + i) * kClipThreads;
+        const bool in = at < tail && at != head;
+        v[i] = in ? ld_nc_v4(base + (size_t)at * 16) : none;
+        o[i] = in ? ld_nc_v4(base + (size_t)at * 16 + 16) : none;
       }
+#pragma unroll
+      for (int i = 0; i < kSumVec; ++i) {
+        const int at = threadIdx.x + (h + i) * kClipThreads;
+        v[i] = shifted(v[i], o[i], off);
+        if (at < n && (at >= tail || at == head)) v[i] = load_each(g + ((int64_t)chunk * kChunkVec + at) * V);
+      }
+      sum += vec_squares<T>(v);
     }
   }
-  // the elements before the first and after the last whole vector
-  if (chunk == 0 && (int)threadIdx.x < head) {
-    const double d = (double)to_f<T>(g[threadIdx.x]);
-    sum += d * d;
-  }
-  if (last) {
-    const int64_t at = head + nvec * V + threadIdx.x;
+  if (last) {                            // the elements after the last whole vector
+    const int64_t at = nvec * V + threadIdx.x;
     if (at < numel) {
       const double d = (double)to_f<T>(g[at]);
       sum += d * d;
@@ -245,11 +303,8 @@ grad_scale_kernel(const __grid_constant__ ClipTable<M> tab, const double* __rest
 
 inline size_t dt_bytes(int dt) { return dt == MOE_F32 ? 4 : 2; }
 
-int64_t chunks_of(const void* g, int64_t numel, int dt) {
-  const int64_t V = 16 / (int64_t)dt_bytes(dt);
-  const int64_t head = (int64_t)(((16u - ((uintptr_t)g & 15u)) & 15u) / dt_bytes(dt));
-  const int64_t nvec = numel > head ? (numel - head) / V : 0;
-  const int64_t c = cdiv(nvec, kChunkVec);
+int64_t chunks_of(int64_t numel, int dt) {
+  const int64_t c = cdiv(numel / (16 / (int64_t)dt_bytes(dt)), kChunkVec);
   return c > 0 ? c : 1;
 }
 
@@ -297,7 +352,7 @@ moe_status clip_run(const void* const* grads, void* const* outs, const int64_t* 
       int64_t chunks = 0;
       while (at < count && tab.count < M) {
         if (numels[at] > 0) {
-          const int64_t c = chunks_of(grads[at], numels[at], dts[at]);
+          const int64_t c = chunks_of(numels[at], dts[at]);
           if (chunks + c > 0x3fffffff) return MOE_ERR_UNSUPPORTED;
           tab.t[tab.count++] = {grads[at], copy ? outs[at] : const_cast<void*>(grads[at]), numels[at],
                                 (int32_t)chunks, dts[at]};

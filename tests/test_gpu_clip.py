@@ -217,3 +217,24 @@ def test_a_norm_past_the_largest_float():
         for o, g in zip(outs, grads):
             want = g.double() * (limit / n)
             assert bool(((o.double() - want).abs() <= want.abs() * 20 * U + torch.finfo(g.dtype).tiny).all())
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 5, 8, 9, 31, 4097, 16384, 300001])
+def test_the_norm_does_not_depend_on_where_the_gradients_lie(n, dt):
+    """Data-parallel ranks may hold the same gradients at other offsets from a 16-byte boundary,
+    and have to scale them by the same bits."""
+    values = [rand((n,), dt, 1), rand((2 * n + 3,), dt, 2), rand((n + 1,), torch.float32, 3)]
+    ref = None
+    for off in range(8):
+        grads = []
+        for i, v in enumerate(values):
+            at = (off * (i + 1)) % 8
+            flat = torch.full((v.numel() + 16,), float("nan"), dtype=v.dtype, device="cuda")   # the neighbours do not count
+            flat[at:at + v.numel()] = v
+            grads.append(flat[at:at + v.numel()])
+        norm = moe.moe_clip_grad_norm(grads, 0.1 * n ** 0.5)
+        check(norm, grads, values, 0.1 * n ** 0.5)
+        got = [norm.clone()] + [g.clone() for g in grads]
+        ref = ref or got
+        assert all(torch.equal(a, b) for a, b in zip(ref, got)), off
