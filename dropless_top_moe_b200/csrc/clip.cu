@@ -309,8 +309,10 @@ int64_t chunks_of(int64_t numel, int dt) {
 }
 
 // Two gradients that share memory, or an output that covers another
-// gradient's input, would be scaled while a second block still reads them.
-bool overlapping(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dts, int count) {
+// gradient's input, would be scaled while a second block still reads them; so would
+// what the call writes besides, the norm and the workspace.
+bool overlapping(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dts, int count,
+                 const void* norm, const void* ws, size_t ws_bytes) {
   struct Range {
     uintptr_t a, b;
     int i;
@@ -319,8 +321,12 @@ bool overlapping(const void* const* grads, void* const* outs, const int64_t* num
   w.reserve(count);
   for (int i = 0; i < count; ++i)
     if (numels[i] > 0) {
-      const uintptr_t a = (uintptr_t)(outs ? outs[i] : grads[i]);
-      w.push_back({a, a + (uintptr_t)numels[i] * dt_bytes(dts[i]), i});
+      const uintptr_t a = (uintptr_t)(outs ? outs[i] : grads[i]), bytes = (uintptr_t)numels[i] * dt_bytes(dts[i]);
+      w.push_back({a, a + bytes, i});
+      for (const uintptr_t p : {a, (uintptr_t)grads[i]})
+        if (((uintptr_t)norm < p + bytes && p < (uintptr_t)norm + sizeof(float)) ||
+            ((uintptr_t)ws < p + bytes && p < (uintptr_t)ws + ws_bytes))
+          return true;
     }
   std::sort(w.begin(), w.end(), [](const Range& p, const Range& q) { return p.a < q.a; });
   for (size_t k = 1; k < w.size(); ++k)
@@ -412,7 +418,8 @@ moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const
   if (((uintptr_t)norm & 3u) || ((uintptr_t)ws & 15u)) return MOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < moe_clip_grad_norm_workspace_size(count)) return MOE_ERR_WORKSPACE;
   try {
-    if (overlapping(grads, outs, numels, dtypes, count)) return MOE_ERR_INVALID_ARG;
+    if (overlapping(grads, outs, numels, dtypes, count, norm, ws, moe_clip_grad_norm_workspace_size(count)))
+      return MOE_ERR_INVALID_ARG;
   } catch (const std::bad_alloc&) {
     return MOE_ERR_UNSUPPORTED;   // no host memory for the check
   }

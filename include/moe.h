@@ -403,7 +403,7 @@ moe_status moe_add_rms_norm_bwd(const void* dy, const void* h, const void* weigh
  * dtypes[i]: a moe_dtype, which may differ from tensor to tensor.
  * outs NULL: in place (nothing is written when f = 1).  outs[i] may be
  * grads[i]; two written ranges that overlap, or one that overlaps another
- * gradient, are MOE_ERR_INVALID_ARG.  Empty tensors are skipped; an empty
+ * gradient, are MOE_ERR_INVALID_ARG, as are norm or ws inside any of them.  Empty tensors are skipped; an empty
  * list has norm 0.
  * max_norm >= 0; infinity only takes the norm.  f comes from the norm in double: of
  * finite gradients whose norm passes the largest float *norm is infinity, and they are

@@ -176,3 +176,19 @@ def test_few_token_tickets_cover_their_line(tmp_path):
                     os.path.join(root, "tests", "c_api", "decode_line.cpp"), "-o", exe], check=True)
     res = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert res.returncode == 0, res.stdout[-2000:]
+
+
+def test_clip_refuses_a_norm_or_workspace_inside_a_gradient(lib):
+    """Both are written by the call: a block would scale, or sum, what another has overwritten."""
+    def clip(norm, ws, outs=None):
+        k = 2
+        return lib.moe_clip_grad_norm((ctypes.c_void_p * k)(A, B), None if outs is None else (ctypes.c_void_p * k)(*outs),
+                                      (ctypes.c_int64 * k)(100, 100), (ctypes.c_int32 * k)(MOE_F32, MOE_BF16), k, 1.0,
+                                      norm, ws, BIG, None)
+    size = lib.moe_clip_grad_norm_workspace_size(2)
+    assert clip(A, D) == INV and clip(A + 396, D) == INV and clip(B + 196, D) == INV
+    assert clip(C, A) == INV and clip(C, A + 384) == INV and clip(C, A - size + 16) == INV and clip(C, B - 256) == INV
+    for outs in ((D, E_), (A, E_)):
+        assert clip(E_ + 100, 9 * A, outs) == INV and clip(outs[0] + 4, 9 * A, outs) == INV
+        assert clip(9 * A, E_ + 192, outs) == INV and clip(9 * A, outs[0] - 256, outs) == INV
+        assert clip(B + 8, 9 * A, outs) == INV                       # a gradient that is only read
