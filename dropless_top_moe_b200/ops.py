@@ -390,6 +390,22 @@ def moe_clip_grad_norm(grads, max_norm: float, outs=None, ws=None, norm=None) ->
     return norm
 
 
+def check_clip(grads, max_norm: float) -> None:
+    """Raise what moe_clip_grad_norm(grads, max_norm) would, in place, before any of them is touched."""
+    if not max_norm >= 0:
+        raise ValueError(f"max_norm: expected a limit of 0 or more, got {max_norm}")
+    for i, g in enumerate(grads):
+        _dt(g)
+        if not g.is_contiguous():
+            raise ValueError(f"grads[{i}]: tensors must be contiguous")
+    spans = sorted((g.data_ptr(), g.data_ptr() + g.numel() * g.element_size(), i) for i, g in enumerate(grads) if g.numel())
+    for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError(f"grads[{i}], grads[{j}]: gradients that are clipped together may share no memory")
+    for i, g in enumerate(grads):
+        _arg(f"grads[{i}]", g, g.shape, g.dtype, grads[0].get_device())
+
+
 def selftest_wait_timeout(status, timeout_ns: int):
     """Run the bounded pipeline wait on a barrier nothing arrives at; after
     timeout_ns it sets MOE_DEVERR_TIMEOUT in status (a device int32 tensor)."""

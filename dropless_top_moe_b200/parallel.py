@@ -24,7 +24,7 @@ import torch
 import torch.distributed as dist
 
 from ._lib import MOE_BF16, MOE_F32, call
-from .ops import moe_clip_grad_norm
+from .ops import check_clip, moe_clip_grad_norm
 
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -47,8 +47,12 @@ def allreduce_grads(tensors: Iterable[torch.Tensor], group: Optional[dist.Proces
     local_sum(recv [world, shard], world, scale, out) is step 2.
     max_norm: then also scale them to a global norm of at most that much
     (moe_clip_grad_norm; every rank holds the same gradients by then, so it scales by
-    the same bits), and return the norm they had."""
+    the same bits), and return the norm they had.  What the clipping refuses (a limit below
+    zero, tensors that share memory or are not on one CUDA device) is refused before
+    anything is reduced."""
     tensors = list(tensors)
+    if max_norm is not None:
+        check_clip(tensors, max_norm)
     _reduce(tensors, group, average, chunk_elems, local_sum)
     return None if max_norm is None else moe_clip_grad_norm(tensors, max_norm)
 

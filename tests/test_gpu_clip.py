@@ -238,3 +238,22 @@ def test_the_norm_does_not_depend_on_where_the_gradients_lie(n, dt):
         got = [norm.clone()] + [g.clone() for g in grads]
         ref = ref or got
         assert all(torch.equal(a, b) for a, b in zip(ref, got)), off
+
+
+def test_the_data_parallel_reduction_refuses_like_the_clipping():
+    """check_clip, which allreduce_grads runs before it reduces, and the clipping agree on what they refuse."""
+    from dropless_top_moe_b200.ops import check_clip
+
+    flat = rand((64,), torch.float32, 1)
+    keep = flat.clone()
+    bad = [([flat[:8], flat[7:16]], 1.0), ([flat, flat], 1.0), ([flat], -0.5), ([flat], math.nan), ([flat[::2]], 1.0),
+           ([flat.cpu()], 1.0), ([flat[:8], flat[8:].cpu()], 1.0), ([flat.half()], 1.0)]
+    for grads, limit in bad:
+        with pytest.raises((ValueError, TypeError)):
+            check_clip(grads, limit)
+        with pytest.raises((ValueError, TypeError, moe.MoEError)):
+            moe.moe_clip_grad_norm(grads, limit)
+    for grads, limit in [([], 1.0), ([flat[:8], flat[8:16], flat[0:0]], 0.0), ([flat], math.inf),
+                         ([flat.bfloat16(), flat[1:]], 1.0)]:
+        check_clip(grads, limit)
+    assert torch.equal(flat, keep)
