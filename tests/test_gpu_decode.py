@@ -297,3 +297,68 @@ def test_many_tokens_on_many_short_tiles(sizes):
     """Tiles of two units, shorter than the length asked of a ticket for that many tokens."""
     N, H, E, K, F = sizes
     run(small_shape("short", N=N, H=H, E=E, K=K, F=F), seed=28)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 3, 21])
+def test_output_over_the_input(N, dtype):
+    """y over x in every kernel: other blocks may still read tokens while some write y."""
+    shape = small_shape("over", N=N, H=256, E=8, K=2, F=512, dtype=dtype)
+    layer, c = run(shape, seed=21)
+    want = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"]).clone()
+    for _ in range(20):
+        x = c["x"].clone()
+        layer.forward(x, c["W_r"], c["W1"], c["W3"], c["W2"], y=x)
+        assert torch.equal(x, want)
+    assert layer.status() == 0
+
+
+def test_layers_of_every_kernel_on_their_own_streams():
+    """Overlapping calls of the direct variant (up to four tokens) with the other kernels."""
+    shapes = [small_shape("a", N=3, H=1024, E=16, K=4, F=1024), small_shape("b", N=1, H=512, E=32, K=6, F=512),
+              small_shape("c", N=30, H=512, E=32, K=4, F=512), small_shape("d", N=4, H=256, E=16, K=2, F=300, dtype="f32")]
+    work = [run(s, seed=22 + i) for i, s in enumerate(shapes)]
+    want = [l.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"]).clone() for l, c in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for _ in range(30):
+        for (l, c), s in zip(work, streams):
+            with torch.cuda.stream(s):
+                l.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"])
+    torch.cuda.synchronize()
+    for (l, c), w in zip(work, want):
+        assert l.status() == 0 and torch.equal(l.y, w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_every_one_of_the_most_experts_is_used(dtype):
+    """256 experts, each with tokens: token n's logits are largest at experts 32 n .. 32 n + 31 (mod 256)."""
+    N, H, E, K, F = 24, 128, 256, 32, 128
+    shape = small_shape("all", N=N, H=H, E=E, K=K, F=F, dtype=dtype)
+    c = make_case(shape, seed=26, with_dy=False, repair=False)
+    c["x"].zero_()
+    for n in range(N):
+        c["x"][n, n % 8] = 1.0
+        c["x"][n, 8:] = torch.randn(H - 8, generator=torch.Generator().manual_seed(n)).to(c["x"])
+    c["W_r"].zero_()
+    for j in range(8):
+        c["W_r"][j, 32 * j:32 * j + 32] = 4.0 + torch.arange(32, device="cuda") / 16
+    c["x_cpu"], c["W_r_cpu"] = c["x"].cpu(), c["W_r"].cpu()
+    layer = moe.MoEDecodeLayer(N, H, E, K, F, dtype=shape.torch_dtype)
+    y = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"])
+    assert torch.unique(layer.top_experts).numel() == E
+    check(layer, c, K, y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [2, 8, 40])
+def test_nothing_of_the_workspace_but_its_head_passes_from_call_to_call(N, dtype):
+    """Whatever an earlier call, or one that gave up, left behind the workspace's first 256 bytes."""
+    shape = small_shape("dirty", N=N, H=256, E=16, K=4, F=384, dtype=dtype)
+    layer, c = run(shape, seed=27)
+    want = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"]).clone()
+    for byte in (0x00, 0x01, 0x7f, 0xff):
+        layer.ws[256:].fill_(byte)
+        y = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"])
+        assert layer.status() == 0 and torch.equal(y, want), byte
+    assert not bool(layer.ws[:256].any())            # the counters between calls are back at zero
