@@ -57,6 +57,7 @@ SIGNATURES = {
     "moe_clip_grad_norm_workspace_size": (SZ, [I32]),
     "moe_clip_grad_norm": (I32, [P, P, P, P, I32, FL, P, P, SZ, P]),
     "moe_selftest_wait_timeout": (I32, [P, I64, P]),
+    "moe_selftest_handover_timeout": (I32, [P, SZ, I64, P, P]),
     "moe_trace_attach": (I32, [P, I32, P, P]),
     "moe_trace_detach": (I32, []),
 }

@@ -198,7 +198,7 @@ __device__ __forceinline__ bool empty(float4 v) {
 }
 // The limit of a thread that polls words.
 struct Patience {
-  uint64_t t0 = 0;
+  uint64_t t0 = 0, limit = kTimeoutNs;
   uint32_t it = 0;
   // another look: false when this thread, or another, gave up
   __device__ __forceinline__ bool again(Counters* cnt, int* status) {
@@ -206,7 +206,7 @@ struct Patience {
     if (*(volatile int*)&cnt->abort) return false;
     const uint64_t now = umma::globaltimer();
     if (t0 == 0) t0 = now;
-    if (now - t0 <= kTimeoutNs) return true;
+    if (now - t0 <= limit) return true;
     *(volatile int*)&cnt->abort = 1;
     raise_status(status, MOE_DEVERR_TIMEOUT);
     return false;
@@ -344,14 +344,15 @@ __device__ __forceinline__ void add_release(int* p, int v) {
   asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 // One thread: until *p reaches `want`; false when it gave up.
-__device__ __forceinline__ bool wait_count(const int* p, int want, Counters* cnt, int* status) {
+__device__ __forceinline__ bool wait_count(const int* p, int want, Counters* cnt, int* status,
+                                           uint64_t limit = kTimeoutNs) {
   if (ld_acquire(p) >= want) return true;
   const uint64_t t0 = umma::globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (ld_acquire(p) >= want) return true;
     if ((it & 63) == 0) {
       if (*(volatile int*)&cnt->abort) return false;
-      if (umma::globaltimer() - t0 > kTimeoutNs) {
+      if (umma::globaltimer() - t0 > limit) {
         *(volatile int*)&cnt->abort = 1;
         raise_status(status, MOE_DEVERR_TIMEOUT);
         return false;

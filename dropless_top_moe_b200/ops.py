@@ -413,6 +413,13 @@ def selftest_wait_timeout(status, timeout_ns: int):
     return status
 
 
+def selftest_handover_timeout(ws, seen, timeout_ns: int):
+    """Run the few-token layer's bounded waits, in a workspace of that layer, on values that nothing writes;
+    seen (a device int32 tensor) tells which gave up, and the workspace's status has MOE_DEVERR_TIMEOUT."""
+    call("moe_selftest_handover_timeout", _p(ws), ws.numel(), int(timeout_ns), _p(seen), _stream())
+    return seen
+
+
 class MoELayer:
     """Whole-layer forward / backward through moe_layer_fwd / moe_layer_bwd.
 

@@ -429,6 +429,16 @@ moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const
  * status or a limit out of range. */
 moe_status moe_selftest_wait_timeout(int32_t* status, int64_t timeout_ns, moe_stream_t stream);
 
+/* The same for moe_layer_decode's waits on what its blocks hand over, in a
+ * workspace of that call: one thread waits on a counter and polls a word that
+ * nothing writes, each until timeout_ns (1 us .. 1 s) has passed, and leaves
+ * MOE_DEVERR_TIMEOUT in the workspace's status word.  *seen (device int32):
+ * 1 = the counter's wait gave up and told the other waits, 2 = a wait so told
+ * ended at once, 4 = the polling gave up.  After moe_workspace_init the
+ * workspace serves the next call. */
+moe_status moe_selftest_handover_timeout(void* ws, size_t ws_bytes, int64_t timeout_ns, int32_t* seen,
+                                         moe_stream_t stream);
+
 /* Per-launch timing.  While attached, every kernel launch made by any entry
  * point records events[2*i] on its stream just before launch i and
  * events[2*i+1] just after it, stores a static kernel name in labels[i]

@@ -14,6 +14,7 @@ import pytest
 import torch
 
 import dropless_top_moe_b200 as moe
+from dropless_top_moe_b200._lib import MOE_DEVERR_TIMEOUT
 from oracle import moe_oracle as om
 from tests._cases import assert_routing, make_case, routing_tol, small_shape
 
@@ -362,3 +363,22 @@ def test_nothing_of_the_workspace_but_its_head_passes_from_call_to_call(N, dtype
         y = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"])
         assert layer.status() == 0 and torch.equal(y, want), byte
     assert not bool(layer.ws[:256].any())            # the counters between calls are back at zero
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [3, 20])
+def test_waits_on_other_blocks_give_up_and_the_workspace_serves_the_next_call(N, dtype):
+    """Every wait on a handed-over value is bounded: it ends with the status bit and tells the others."""
+    shape = small_shape("giveup", N=N, H=256, E=16, K=4, F=384, dtype=dtype)
+    layer, c = run(shape, seed=29)
+    want = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"]).clone()
+    seen = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.selftest_handover_timeout(layer.ws, seen, 5_000_000)       # 5 ms each
+    torch.cuda.synchronize()
+    assert int(seen) == 7 and layer.status() == MOE_DEVERR_TIMEOUT
+    # the status stays for whoever asks, and the next call is right all the same
+    y = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"])
+    assert layer.status() == MOE_DEVERR_TIMEOUT and torch.equal(y, want)
+    moe.ops.call("moe_workspace_init", layer.ws.data_ptr(), layer.ws.numel(), torch.cuda.current_stream().cuda_stream)
+    y = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"])
+    assert layer.status() == 0 and torch.equal(y, want)

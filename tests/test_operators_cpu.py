@@ -192,3 +192,10 @@ def test_clip_refuses_a_norm_or_workspace_inside_a_gradient(lib):
         assert clip(E_ + 100, 9 * A, outs) == INV and clip(outs[0] + 4, 9 * A, outs) == INV
         assert clip(9 * A, E_ + 192, outs) == INV and clip(9 * A, outs[0] - 256, outs) == INV
         assert clip(B + 8, 9 * A, outs) == INV                       # a gradient that is only read
+
+
+def test_handover_selftest_refuses(lib):
+    st = lib.moe_selftest_handover_timeout
+    assert st(None, BIG, 10 ** 6, A, None) == INV and st(A, BIG, 10 ** 6, None, None) == INV
+    assert st(A + 4, BIG, 10 ** 6, B, None) == INV and st(A, 1000, 10 ** 6, B, None) == WS
+    assert st(A, BIG, 10, B, None) == INV and st(A, BIG, 2 * 10 ** 9, B, None) == INV
