@@ -264,10 +264,11 @@ __device__ __forceinline__ void chunk_scale_tiny(const T* g, T* out, int64_t num
 }
 
 // The norm from the blocks' sums (in a fixed order, the same in every block),
-// then the scaling.  copy: the outputs are other buffers, written for f = 1 too.
+// then the scaling.  The sums are still being written when this kernel starts: no restrict and no
+// read-only path for them.  copy: the outputs are other buffers, written for f = 1 too.
 template <int M>
 __global__ void __launch_bounds__(kClipThreads)
-grad_scale_kernel(const __grid_constant__ ClipTable<M> tab, const double* __restrict__ part, int n_part,
+grad_scale_kernel(const __grid_constant__ ClipTable<M> tab, const double* part, int n_part,
                   float max_norm, int copy, float* norm_out) {
   __shared__ double red[kClipThreads / 32];
   double sum = 0.0;

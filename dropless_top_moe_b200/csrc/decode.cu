@@ -232,7 +232,8 @@ static_assert(sizeof(((Smem*)0)->ring) >= 8 * kTokens * 2 * 64 * sizeof(float), 
 
 // A tile of NM matrices for TM tokens from row t0 of a slot on:
 // C_m[t][c] = sum_r in(t)[r] W_m[r][c]; put(t, c, sums) takes them.  POLL: the words that
-// `in` points to may still be empty.
+// `in` points to may still be empty.  Those of x are not read through the read-only path: y may be written
+// over x, by blocks that are done with a token, while others still read.
 template <int CT, bool WIDE, bool POLL, int NM, int TM, class In, class Put>
 __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, Smem& sm, const float* const (&W)[NM],
                                             int depth, int cols, int c0, int t0, int cnt, In in, Put put) {
@@ -305,7 +306,7 @@ __device__ __forceinline__ void tile_tokens(const Args& a, Patience& patience, S
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[j] = 0.f;
-          if (e0 + j * STEP < rows) v[j] = POLL ? ld_word(row + e0 + j * STEP) : __ldg(row + e0 + j * STEP);
+          if (e0 + j * STEP < rows) v[j] = POLL ? ld_word(row + e0 + j * STEP) : row[e0 + j * STEP];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

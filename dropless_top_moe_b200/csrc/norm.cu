@@ -249,10 +249,11 @@ add_rms_norm_bwd_kernel(const T* dy, const T* h, const T* __restrict__ weight, c
 }
 
 // dw[c] = sum over the blocks' partial rows: kDwRows strided sums, eight loads of
-// each in flight, then those in a fixed order.
+// each in flight, then those in a fixed order.  The partials are still being written when this
+// kernel starts: no restrict and no read-only path for them.
 template <typename T>
 __global__ void __launch_bounds__(kDwCols * kDwRows)
-rms_norm_dw_kernel(const float* __restrict__ part, int G, int H, T* __restrict__ dw) {
+rms_norm_dw_kernel(const float* part, int G, int H, T* __restrict__ dw) {
   static_assert(kDwCols == 8 && kDwRows % 4 == 0, "four rows of eight columns a warp");
   __shared__ float red[kDwRows / 4][kDwCols];
   const int tc = threadIdx.x % kDwCols, tr = threadIdx.x / kDwCols;
