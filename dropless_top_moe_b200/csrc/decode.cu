@@ -181,8 +181,10 @@ decode_route_kernel(const Args a, int S, int wide, int pick) {
 // memory kAhead rows ahead (cp.async): they keep coming across the barriers around the
 // tokens' staging, and need no barrier themselves.  Activations and expert outputs are
 // handed over as words that are their own flags, tiles as tickets in order, so
-// the phases run into each other.  HBM bounds it up to some eight tokens an expert,
-// FMAs beyond.
+// the phases run into each other.  HBM bounds it with few tokens an expert; beyond, every
+// chunk of kTokens tokens passes over its expert's weights again, from L2, and nothing is full:
+// 50 tokens 824/33/7/918 (142 us, floor 46) keep 15 warps an SM that issue in 52 % of the
+// cycles, the FMA pipe 34 % busy, DRAM 28 %.
 constexpr int kThreads = 256;
 constexpr int kXRows = 512;          // rows of the tokens' operand staged at a time
 constexpr int kTokens = 8;           // most tokens at a time
@@ -202,7 +204,7 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
 }
 
 // two sums in one instruction: c = a * b + c, each rounded as fmaf's (1 to 4 % of a layer's time,
-// most with many tokens an expert: issue slots bound it there)
+// most with many tokens an expert)
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
   uint64_t v;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));

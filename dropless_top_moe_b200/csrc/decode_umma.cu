@@ -17,9 +17,10 @@
 // tile leaves fp32 partial sums: of gate and up, the piece that arrives last adds
 // the pieces in order and applies SwiGLU; of the down product, the weighted sum
 // over the experts adds them in order while it reads them.  No sum depends on the
-// order in which blocks run.  Measured: 8 tokens 4096/64/4/2048 (26 experts, 1.3 GB of
-// weights) 198 us, 6.5 TB/s over the whole call; 64 tokens 4096/8/2/14336 444 us, 6.4 TB/s;
-// 1 token 2048/64/6/1408 (104 MB) 30 us, of which 16 are the weights.
+// order in which blocks run.  Measured, a call among others: 8 tokens 4096/64/4/2048 (26 experts,
+// 1.3 GB of weights) 195 to 211 us from GPU to GPU, 6.2 to 6.7 TB/s over the whole call; 64 tokens
+// 4096/8/2/14336 432 to 451 us; 1 token 2048/64/6/1408 (104 MB) 30 to 33 us, of which 16
+// are the weights.
 //
 // The activations pass to the down product as two bf16 numbers, the rounded value
 // and what the rounding left, and y is as exact as with fp32 activations (relative
