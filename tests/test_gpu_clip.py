@@ -257,3 +257,15 @@ def test_the_data_parallel_reduction_refuses_like_the_clipping():
                          ([flat.bfloat16(), flat[1:]], 1.0)]:
         check_clip(grads, limit)
     assert torch.equal(flat, keep)
+
+
+def test_some_outputs_in_place_and_others_not():
+    grads = [rand((5000 + i,), [torch.float32, torch.bfloat16][i % 2], i) for i in range(6)]
+    keep = [g.clone() for g in grads]
+    outs = [g if i % 3 == 0 else torch.empty_like(g) for i, g in enumerate(grads)]
+    n = norm64(keep)
+    for limit in (0.2 * n, 2 * n):
+        for g, k in zip(grads, keep):
+            g.copy_(k)
+        check(moe.moe_clip_grad_norm(grads, limit, outs=outs), outs, keep, limit)
+        assert all(torch.equal(g, k) for i, (g, k) in enumerate(zip(grads, keep)) if i % 3)

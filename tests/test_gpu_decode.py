@@ -382,3 +382,31 @@ def test_waits_on_other_blocks_give_up_and_the_workspace_serves_the_next_call(N,
     moe.ops.call("moe_workspace_init", layer.ws.data_ptr(), layer.ws.numel(), torch.cuda.current_stream().cuda_stream)
     y = layer.forward(c["x"], c["W_r"], c["W1"], c["W3"], c["W2"])
     assert layer.status() == 0 and torch.equal(y, want)
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of one layer, of different sizes and kernels, replayed in turn on one stream."""
+    shape = small_shape("graphs", N=70, H=256, E=16, K=4, F=384)
+    layer, c = run(shape, seed=30)
+    args = (c["W_r"], c["W1"], c["W3"], c["W2"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    calls = []
+    for n in (3, 70, 20):
+        x, y = c["x"][:n].clone(), torch.empty(n, 256, dtype=torch.bfloat16, device="cuda")
+        want = layer.forward(x, *args).clone()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+            layer.forward(x, *args, y=y)
+        calls.append((graph, y, want, x))               # the graph reads x: it has to live
+    for i in range(30):
+        graph, y, want, _ = calls[(i * i + i // 4) % 3]
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+    for call in calls * 5:                              # back to back
+        call[0].replay()
+    torch.cuda.synchronize()
+    assert layer.status() == 0 and all(torch.equal(y, want) for _, y, want, _ in calls)

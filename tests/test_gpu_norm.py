@@ -239,3 +239,27 @@ def test_in_place_without_a_residual_has_no_h_to_give(dtype):
     x = keep.clone()
     y, h = moe.moe_add_rms_norm(x, w, residual=r, eps=EPS, y=x)        # with a residual h has a buffer of its own
     check_forward(y, h, keep, r, w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_every_way_in_place(dtype):
+    """h over x or residual, y over the other, either alone, x and residual the same tensor."""
+    dt = DT[dtype]
+    N, H = 700, 1024
+    x0, r0, w = rand((N, H), dt, 1), rand((N, H), dt, 2), rand((H,), dt, 3)
+    want = moe.moe_add_rms_norm(x0, w, residual=r0, eps=EPS)
+    for hs, ys in (("x", "r"), ("r", "x"), ("x", None), ("r", None), (None, "x"), (None, "r")):
+        t = {"x": x0.clone(), "r": r0.clone(), None: None}
+        y, h = moe.moe_add_rms_norm(t["x"], w, residual=t["r"], eps=EPS, y=t[ys], h=t[hs])
+        assert torch.equal(y, want[0]) and torch.equal(h, want[1]), (hs, ys)
+    want = moe.moe_add_rms_norm(x0, w, residual=x0, eps=EPS)
+    check_forward(*want, x0, x0, w)
+    for which in ("h", "y"):
+        t = x0.clone()
+        y, h = moe.moe_add_rms_norm(t, w, residual=t, eps=EPS, **{which: t})
+        assert torch.equal(y, want[0]) and torch.equal(h, want[1]), which
+    dy = rand((N, H), dt, 4)
+    want = moe.moe_add_rms_norm_bwd(dy, x0, w, dh=dy, eps=EPS)
+    check_backward(*want, dy, x0, w, dy)
+    got = moe.moe_add_rms_norm_bwd(dy, x0, w, dh=dy, eps=EPS, dx=dy)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
