@@ -123,6 +123,13 @@ __device__ __forceinline__ bool epi_all(bool yes) {
   return r != 0;
 }
 
+// A warp after its lane 0 has waited: what lane 0 has seen is ordered before what the other lanes go on
+// to write or copy (a shuffle alone orders no memory).
+__device__ __forceinline__ bool lane0_says(bool ok) {
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+}
+
 struct Shared {
   Plan plan;
   int tokens[kMaxTokens];      // warp 1's current slot
@@ -320,7 +327,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
           mbar_arrive(bar(sm.ring_full[slot]));
         }
       }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      ok = lane0_says(ok);
       if (!ok) break;
       const Ticket k = read_ticket(__shfl_sync(0xffffffffu, v, 0), up, down);
       if (k.stop) break;
@@ -340,7 +347,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
               ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
               if (ok) mbar_expect_tx(bar(sm.full[stage]), kABytes);
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            ok = lane0_says(ok);
             if (!ok) break;
             if (lane < 4)
               tma_load_3d(base + stage * stage_bytes + lane * 8192, m, bar(sm.full[stage]), c, (pc.k0 + i) * kKB, e);
@@ -377,7 +384,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
     int have = -1;                     // slot whose activations are known to be complete
     while (ok) {
       if (lane == 0) ok = mbar_wait_bounded(bar(sm.ring_full[slot]), ring_phase, abort_flag, a.status, kTimeoutNs);
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      ok = lane0_says(ok);
       if (!ok) break;
       const Ticket k = read_ticket(*(volatile int*)&sm.ring[slot], up, down);
       __syncwarp();
@@ -412,7 +419,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
             ok = wait_count(a.cnt->done_act + u, up.nj, a.cnt, a.status);
             if (!ok) *abort_flag = 1;
           }
-          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          ok = lane0_says(ok);
           if (!ok) break;
           fence_proxy_async_global();                      // written by other threads, read by TMA
           have = u;
@@ -478,7 +485,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
                   }
               }
               if (lane == 0) ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
-              ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+              ok = lane0_says(ok);
               if (!ok) break;
               const uint32_t dst = base + stage * stage_bytes + kABytes;
 #pragma unroll
@@ -499,7 +506,7 @@ decode_umma_kernel(const __grid_constant__ Params p) {
             ok = mbar_wait_bounded(bar(sm.empty[stage]), phase ^ 1u, abort_flag, a.status, kTimeoutNs);
             if (ok) mbar_expect_tx(bar(sm.full[stage]), rows * 128);
           }
-          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          ok = lane0_says(ok);
           if (!ok) break;
           const uint32_t dst = base + stage * stage_bytes + kABytes;
           const int kcol = (pc.k0 + i) * kKB;
