@@ -18,8 +18,8 @@
 // the pieces in order and applies SwiGLU; of the down product, the weighted sum
 // over the experts adds them in order while it reads them.  No sum depends on the
 // order in which blocks run.  Measured, a call among others: 8 tokens 4096/64/4/2048 (26 experts,
-// 1.3 GB of weights) 195 to 211 us from GPU to GPU, 6.2 to 6.7 TB/s over the whole call; 64 tokens
-// 4096/8/2/14336 432 to 451 us; 1 token 2048/64/6/1408 (104 MB) 30 to 33 us, of which 16
+// 1.3 GB of weights) 195 to 216 us by the experts used, 6.2 to 6.7 TB/s over the whole call; 64 tokens
+// 4096/8/2/14336 432 to 453 us; 1 token 2048/64/6/1408 (104 MB) 30 to 33 us, of which 16
 // are the weights.
 //
 // The activations pass to the down product as two bf16 numbers, the rounded value
